@@ -17,6 +17,16 @@ Entry points (same names as the C ABI):
   attn_decode_workspace_bytes(B, H, d, num_splits)
   attn_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale, num_splits,
                     workspace)                        paged-KV split-KV decode
+  attn_page_tables(ctx_lens, new_lens, free_pages, free_head, free_head_out, block_table,
+                   seq_lens, cu_q, slot_map, page_size, num_pages)  pages and slots of a step
+  attn_paged_append(k, v, slot_map, k_cache, v_cache, k_bounds)  K/V write and page key bounds
+  attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, seq_lens, o, lse, causal, scale,
+                 workspace)                 attention of new tokens over a paged cache, grouped heads
+  attn_page_select(q, k_bounds, block_table, cu_q, seq_lens, sel, page_size, keep_first,
+                   keep_last, workspace)    the pages each token reads, by a bound of its scores
+  attn_sparse_paged(q, k_cache, v_cache, block_table, cu_q, seq_lens, sel, o, lse, scale,
+                    workspace)              attention over those pages
+  attn_fwd_paged_workspace_bytes(d), attn_page_select_workspace_bytes(T, Hkv, max_pages)
   attn_status(stream) / attn_strerror(code)
 Tensor arguments are torch tensors on the current CUDA device (bf16 for
 q/k/v/o, fp32 for lse and partials, contiguous); ``stream`` defaults to torch's
@@ -74,6 +84,21 @@ lib.attn_bwd.restype = _i
 lib.attn_bwd.argtypes = [_vp] * 9 + [_i] * 6 + [_f, _vp, _sz, _vp]
 lib.attn_bwd_deterministic.restype = _i
 lib.attn_bwd_deterministic.argtypes = lib.attn_bwd.argtypes
+_ll = ctypes.c_longlong
+lib.attn_page_tables.restype = _i
+lib.attn_page_tables.argtypes = [_vp] * 9 + [_i] * 6 + [_vp]
+lib.attn_paged_append.restype = _i
+lib.attn_paged_append.argtypes = [_vp] * 6 + [_i] * 3 + [_ll] + [_i] * 2 + [_vp]
+lib.attn_fwd_paged_workspace_bytes.restype = _sz
+lib.attn_fwd_paged_workspace_bytes.argtypes = [_i]
+lib.attn_fwd_paged.restype = _i
+lib.attn_fwd_paged.argtypes = [_vp] * 8 + [_i] * 5 + [_ll] + [_i] * 4 + [_f, _vp, _sz, _vp]
+lib.attn_page_select_workspace_bytes.restype = _sz
+lib.attn_page_select_workspace_bytes.argtypes = [_i] * 3
+lib.attn_page_select.restype = _i
+lib.attn_page_select.argtypes = [_vp] * 6 + [_i] * 8 + [_ll] + [_i] * 3 + [_vp, _sz, _vp]
+lib.attn_sparse_paged.restype = _i
+lib.attn_sparse_paged.argtypes = [_vp] * 9 + [_i] * 6 + [_ll] + [_i] * 3 + [_f, _vp, _sz, _vp]
 lib.attn_status.restype = _i
 lib.attn_status.argtypes = [_vp]
 
@@ -269,6 +294,167 @@ def attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, causal: bool, scale: float, work
               float(scale), ctypes.c_void_p(workspace.data_ptr()),
               workspace.numel() * workspace.element_size(), _stream(stream)),
            "attn_bwd_deterministic" if deterministic else "attn_bwd")
+
+
+# ---- serving on a paged cache. These calls run on the device of their tensors,
+# whichever is current, on `stream` or that device's current stream.
+
+def _on_device(fn, what: str, tensors, args, stream) -> None:
+    import torch
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError(f"{what}: all tensors must be on one CUDA device")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            code = fn(*args, _stream(stream))
+    else:
+        code = fn(*args, _stream(stream))
+    _check(code, what)
+
+
+def _rows(t, name: str):
+    """Pointer and row stride of a bf16 [T, H, d] tensor whose rows are dense."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D CUDA tensor of torch.bfloat16")
+    T, H, d = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and H > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (H * d if T == 1 else s0)
+
+
+def attn_page_tables(ctx_lens, new_lens, free_pages, free_head, free_head_out, block_table,
+                     seq_lens, cu_q, slot_map, page_size: int, num_pages: int,
+                     stream=None) -> None:
+    """Pages and slots of one step. ctx_lens, new_lens, seq_lens [B], free_pages [F], free_head,
+    free_head_out [1], block_table [B,max_pages], cu_q [B+1] int32; slot_map [T] int64.
+    free_head_out may be free_head, and seq_lens may be ctx_lens."""
+    import torch
+    B = ctx_lens.shape[0]
+    if ctx_lens.dim() != 1 or tuple(new_lens.shape) != (B,) or tuple(seq_lens.shape) != (B,) \
+            or tuple(cu_q.shape) != (B + 1,) or block_table.dim() != 2 \
+            or block_table.shape[0] != B or free_pages.dim() != 1 or slot_map.dim() != 1 \
+            or free_head.numel() != 1 or free_head_out.numel() != 1:
+        raise ValueError("attn_page_tables: inconsistent shapes")
+    i32 = torch.int32
+    _on_device(lib.attn_page_tables, "attn_page_tables",
+               (ctx_lens, new_lens, free_pages, free_head, free_head_out, block_table, seq_lens,
+                cu_q, slot_map),
+               (_tensor(ctx_lens, i32, "ctx_lens"), _tensor(new_lens, i32, "new_lens"),
+                _tensor(free_pages, i32, "free_pages"), _tensor(free_head, i32, "free_head"),
+                _tensor(free_head_out, i32, "free_head_out"),
+                _tensor(block_table, i32, "block_table"), _tensor(seq_lens, i32, "seq_lens"),
+                _tensor(cu_q, i32, "cu_q"), _tensor(slot_map, torch.int64, "slot_map"), B,
+                slot_map.shape[0], free_pages.shape[0], int(page_size), block_table.shape[1],
+                int(num_pages)), stream)
+
+
+def attn_paged_append(k, v, slot_map, k_cache, v_cache, k_bounds=None, stream=None) -> None:
+    """K and V of a step into the cache. k, v [T,Hkv,d] bf16 (rows any one stride apart);
+    slot_map [T] int64; caches [num_pages,Hkv,page_size,d] bf16; k_bounds
+    [num_pages,Hkv,2,d] bf16 or None."""
+    import torch
+    bf16 = torch.bfloat16
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    T, Hkv, d = k.shape
+    P, H2, page_size, d2 = k_cache.shape
+    if v.shape != k.shape or vs != ks or H2 != Hkv or d2 != d or v_cache.shape != k_cache.shape \
+            or tuple(slot_map.shape) != (T,) \
+            or (k_bounds is not None and tuple(k_bounds.shape) != (P, Hkv, 2, d)):
+        raise ValueError("attn_paged_append: inconsistent shapes")
+    tensors = (k, v, slot_map, k_cache, v_cache) + (() if k_bounds is None else (k_bounds,))
+    _on_device(lib.attn_paged_append, "attn_paged_append", tensors,
+               (kp, vp, _tensor(slot_map, torch.int64, "slot_map"),
+                _tensor(k_cache, bf16, "k_cache"), _tensor(v_cache, bf16, "v_cache"),
+                None if k_bounds is None else _tensor(k_bounds, bf16, "k_bounds"), T, Hkv, d, ks,
+                page_size, P), stream)
+
+
+def attn_fwd_paged_workspace_bytes(d: int) -> int:
+    return int(lib.attn_fwd_paged_workspace_bytes(d))
+
+
+def attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, seq_lens, o, lse, causal: bool,
+                   scale: float, workspace, stream=None) -> None:
+    """Attention of new tokens over a paged cache. q [T,Hq,d] bf16 (rows any one stride apart),
+    caches [num_pages,Hkv,page_size,d] bf16, block_table [B,max_pages], cu_q [B+1], seq_lens [B]
+    int32; o [T,Hq,d] bf16, lse [T,Hq] fp32; workspace: uint8, attn_fwd_paged_workspace_bytes(d)."""
+    import torch
+    bf16, i32 = torch.bfloat16, torch.int32
+    qp, qs = _rows(q, "q")
+    T, Hq, d = q.shape
+    P, Hkv, page_size, d2 = k_cache.shape
+    B = seq_lens.shape[0]
+    if d2 != d or v_cache.shape != k_cache.shape or block_table.dim() != 2 \
+            or block_table.shape[0] != B or tuple(cu_q.shape) != (B + 1,) or seq_lens.dim() != 1 \
+            or o.shape != q.shape or tuple(lse.shape) != (T, Hq):
+        raise ValueError("attn_fwd_paged: inconsistent shapes")
+    _on_device(lib.attn_fwd_paged, "attn_fwd_paged",
+               (q, k_cache, v_cache, block_table, cu_q, seq_lens, o, lse, workspace),
+               (qp, _tensor(k_cache, bf16, "k_cache"), _tensor(v_cache, bf16, "v_cache"),
+                _tensor(block_table, i32, "block_table"), _tensor(cu_q, i32, "cu_q"),
+                _tensor(seq_lens, i32, "seq_lens"), _tensor(o, bf16, "o"),
+                _tensor(lse, torch.float32, "lse"), B, T, Hq, Hkv, d, qs, page_size,
+                block_table.shape[1], P, int(bool(causal)), float(scale),
+                _tensor(workspace, torch.uint8, "workspace"), workspace.numel()), stream)
+
+
+def attn_page_select_workspace_bytes(T: int, Hkv: int, max_pages: int) -> int:
+    return int(lib.attn_page_select_workspace_bytes(T, Hkv, max_pages))
+
+
+def attn_page_select(q, k_bounds, block_table, cu_q, seq_lens, sel, page_size: int,
+                     keep_first: int, keep_last: int, workspace, stream=None) -> None:
+    """The sel.shape[2] pages each token and K/V head reads. q [T,Hq,d] bf16 (rows any one stride
+    apart), k_bounds [num_pages,Hkv,2,d] bf16, block_table [B,max_pages], cu_q [B+1], seq_lens
+    [B], sel [T,Hkv,K] int32; workspace: uint8, attn_page_select_workspace_bytes(...)."""
+    import torch
+    i32 = torch.int32
+    qp, qs = _rows(q, "q")
+    T, Hq, d = q.shape
+    P, Hkv, two, d2 = k_bounds.shape
+    B = seq_lens.shape[0]
+    if two != 2 or d2 != d or block_table.dim() != 2 or block_table.shape[0] != B \
+            or tuple(cu_q.shape) != (B + 1,) or seq_lens.dim() != 1 or sel.dim() != 3 \
+            or tuple(sel.shape[:2]) != (T, Hkv):
+        raise ValueError("attn_page_select: inconsistent shapes")
+    _on_device(lib.attn_page_select, "attn_page_select",
+               (q, k_bounds, block_table, cu_q, seq_lens, sel, workspace),
+               (qp, _tensor(k_bounds, torch.bfloat16, "k_bounds"),
+                _tensor(block_table, i32, "block_table"), _tensor(cu_q, i32, "cu_q"),
+                _tensor(seq_lens, i32, "seq_lens"), _tensor(sel, i32, "sel"), B, T, Hq, Hkv, d,
+                sel.shape[2], int(keep_first), int(keep_last), qs, int(page_size),
+                block_table.shape[1], P, _tensor(workspace, torch.uint8, "workspace"),
+                workspace.numel()), stream)
+
+
+def attn_sparse_paged(q, k_cache, v_cache, block_table, cu_q, seq_lens, sel, o, lse,
+                      scale: float, workspace, stream=None) -> None:
+    """attn_fwd_paged (causal) over the pages listed in sel [T,Hkv,K] int32 (-1: none)."""
+    import torch
+    bf16, i32 = torch.bfloat16, torch.int32
+    qp, qs = _rows(q, "q")
+    T, Hq, d = q.shape
+    P, Hkv, page_size, d2 = k_cache.shape
+    B = seq_lens.shape[0]
+    if d2 != d or v_cache.shape != k_cache.shape or block_table.dim() != 2 \
+            or block_table.shape[0] != B or tuple(cu_q.shape) != (B + 1,) or seq_lens.dim() != 1 \
+            or o.shape != q.shape or tuple(lse.shape) != (T, Hq) or sel.dim() != 3 \
+            or tuple(sel.shape[:2]) != (T, Hkv):
+        raise ValueError("attn_sparse_paged: inconsistent shapes")
+    _on_device(lib.attn_sparse_paged, "attn_sparse_paged",
+               (q, k_cache, v_cache, block_table, cu_q, seq_lens, sel, o, lse, workspace),
+               (qp, _tensor(k_cache, bf16, "k_cache"), _tensor(v_cache, bf16, "v_cache"),
+                _tensor(block_table, i32, "block_table"), _tensor(cu_q, i32, "cu_q"),
+                _tensor(seq_lens, i32, "seq_lens"), _tensor(sel, i32, "sel"),
+                _tensor(o, bf16, "o"), _tensor(lse, torch.float32, "lse"), B, T, Hq, Hkv, d,
+                sel.shape[2], qs, page_size, block_table.shape[1], P, float(scale),
+                _tensor(workspace, torch.uint8, "workspace"), workspace.numel()), stream)
 
 
 def attn_status(stream=None) -> int:

@@ -67,12 +67,16 @@ FWD_LAUNCH_REGS = 168
 # launch the P/dS warpgroups' increase would wait forever, and more would not
 # fit five warps per SM scheduler, so the build requires exactly this count.
 BWD_LAUNCH_REGS = 96
+# The paged forward redistributes registers as the prefill kernel does, from the
+# same 384 threads (PagedTraits::kLaunchRegs).
+PAGED_LAUNCH_REGS = 168
 
 
 def check_register_budget(ptxas_log: str, lib: str = LIB) -> None:
     current = None
     seen = 0
     seen_bwd = 0
+    seen_paged = 0
     for line in ptxas_log.splitlines():
         m = re.search(r"Compiling entry function '([^']+)'", line)
         if m:
@@ -85,15 +89,21 @@ def check_register_budget(ptxas_log: str, lib: str = LIB) -> None:
                 os.remove(lib)
                 raise RuntimeError(f"{current} uses {m.group(1)} registers, expected "
                                    f"{BWD_LAUNCH_REGS}: the setmaxnreg split would not fit")
+        if m and current and "attn_paged_sm100_kernel" in current:
+            seen_paged += 1
+            if int(m.group(1)) != PAGED_LAUNCH_REGS:
+                os.remove(lib)
+                raise RuntimeError(f"{current} uses {m.group(1)} registers, expected "
+                                   f"{PAGED_LAUNCH_REGS}: the setmaxnreg split would not fit")
         if m and current and "attn_fwd_sm100_kernel" in current:
             seen += 1
             if int(m.group(1)) != FWD_LAUNCH_REGS:
                 os.remove(lib)
                 raise RuntimeError(f"{current} uses {m.group(1)} registers, expected "
                                    f"{FWD_LAUNCH_REGS}: the setmaxnreg split would not fit")
-    if seen == 0 or seen_bwd == 0:
+    if seen == 0 or seen_bwd == 0 or seen_paged == 0:
         os.remove(lib)
-        raise RuntimeError("ptxas register report for the prefill or backward kernel not found")
+        raise RuntimeError("ptxas register report for the prefill, backward or paged kernel not found")
 
 
 if __name__ == "__main__":

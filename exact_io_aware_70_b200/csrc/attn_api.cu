@@ -26,6 +26,8 @@ __device__ unsigned g_attn_status = 0;
 #include "bwd_sm100.cuh"
 #include "decode_sm100.cuh"
 #include "fwd_sm100.cuh"
+#include "paged_cache_sm100.cuh"
+#include "paged_fwd_sm100.cuh"
 
 using namespace eattn;
 
@@ -107,8 +109,28 @@ bool encode_u8_map(CUtensorMap* map, const void* base, int BH, int N, int D) {
     return r == CUDA_SUCCESS;
 }
 
+// Tensor map over q viewed as [T][Hq][D] with `stride` elements from row to row;
+// box = `tokens` rows x the `heads` query heads of a group x 64 columns.
+bool encode_q_map(CUtensorMap* map, const void* base, int T, int Hq, int D, long long stride,
+                  int heads, int tokens) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 struct DeviceInfo {
     int sms = 0;
+    bool paged_attr_set[4] = {false, false, false, false};
+    bool tables_attr_set = false;
+    bool score_attr_set[2] = {false, false};
     bool fwd_attr_set[8] = {false, false, false, false, false, false, false, false};
     bool bwd_attr_set[4] = {false, false, false, false};
 };
@@ -636,6 +658,339 @@ attn_status_t attn_status(void* stream) {
     if (word & kDevErrIndexCheck) return ATTN_ERR_INDEX_CHECK;
     if (word & kDevErrBadIndex) return ATTN_ERR_BAD_INDEX;
     return ATTN_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------ serving on a paged cache --
+namespace {
+
+// Checks shared by the entry points that take a paged cache's geometry.
+attn_status_t check_pages(int B, int Hkv, int d, int page_size, int max_pages, int num_pages) {
+    if (B < 1 || Hkv < 1 || B > (1 << 24) || Hkv > 65535) return ATTN_ERR_INVALID_ARG;
+    if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (max_pages < 1 || num_pages < 1) return ATTN_ERR_INVALID_ARG;
+    if ((long long)max_pages * page_size > kMaxSeq) return ATTN_ERR_INVALID_ARG;
+    // the caches' rows of pages and heads are 32-bit tensor-map coordinates
+    if ((long long)num_pages * Hkv >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+    if ((long long)num_pages * Hkv * page_size * 128 > (1ll << 46)) return ATTN_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+int shift_of(int page_size) {
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int D, bool SPARSE>
+attn_status_t launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const PagedParams& p, cudaStream_t stream) {
+    using T = PagedTraits<D>;
+    const int dev = current_device();
+    if (dev < 0 || dev >= 64) return ATTN_ERR_CUDA;
+    auto kern = attn_paged_sm100_kernel<D, SPARSE>;
+    int sms;
+    {
+        std::lock_guard<std::mutex> lk(g_dev_mu);
+        DeviceInfo& di = g_dev[dev];
+        if (di.sms == 0 &&
+            cudaDeviceGetAttribute(&di.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return ATTN_ERR_CUDA;
+        const int slot = (SPARSE ? 2 : 0) + (D == 128 ? 1 : 0);
+        if (!di.paged_attr_set[slot]) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     T::kSmemBytes) != cudaSuccess)
+                return ATTN_ERR_CUDA;
+            di.paged_attr_set[slot] = true;
+        }
+        sms = di.sms;
+    }
+    const int grid = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
+    kern<<<grid, kPagedThreads, T::kSmemBytes, stream>>>(tq, tk, tv, p);
+    attn_paged_merge_kernel<D><<<dim3(grid, 256 * D / 4 / kPagedMergeThreads), kPagedMergeThreads,
+                                 0, stream>>>(p, grid);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// attn_fwd_paged, and attn_sparse_paged (sel not null)
+attn_status_t paged_entry(const void* q, const void* k_cache, const void* v_cache,
+                          const int* block_table, const int* cu_q, const int* seq_lens,
+                          const int* sel, int K, void* o, float* lse, int B, int T, int Hq,
+                          int Hkv, int d, long long q_stride, int page_size, int max_pages,
+                          int num_pages, int causal, float scale, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    if (!q || !k_cache || !v_cache || !block_table || !cu_q || !seq_lens || !o || !lse ||
+        !workspace)
+        return ATTN_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+    attn_status_t s = check_pages(B, Hkv, d, page_size, max_pages, num_pages);
+    if (s != ATTN_OK) return s;
+    if (T < 1 || T > (1 << 30) || Hq < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+    const int G = Hq / Hkv;
+    if (G > 128) return ATTN_ERR_UNSUPPORTED;
+    if (q_stride < (long long)Hq * d || q_stride > (1ll << 36)) return ATTN_ERR_INVALID_ARG;
+    if (sel) {
+        if (K < 1) return ATTN_ERR_INVALID_ARG;
+        const int runs = page_size > 128 ? page_size / 128 : 1;   // list entries of a page
+        if ((long long)K * runs > kPagedListMax) return ATTN_ERR_UNSUPPORTED;
+        if (!aligned(sel, 4)) return ATTN_ERR_ALIGNMENT;
+    }
+    if (workspace_bytes < attn_fwd_paged_workspace_bytes(d)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
+        !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(cu_q, 4) ||
+        !aligned(seq_lens, 4) || !aligned(workspace, 256) || q_stride % 8 != 0)
+        return ATTN_ERR_ALIGNMENT;
+
+    PagedParams p;
+    p.tpt = sel ? 1 : 128 / G;
+    const int box = page_size < 128 ? page_size : 128;
+    CUtensorMap tq, tk, tv;
+    if (!encode_q_map(&tq, q, T, Hq, d, q_stride, G, p.tpt) ||
+        !encode_bf16_map(&tk, k_cache, num_pages * Hkv, page_size, d, box) ||
+        !encode_bf16_map(&tv, v_cache, num_pages * Hkv, page_size, d, box))
+        return ATTN_ERR_CUDA;
+    char* ws = static_cast<char*>(workspace);
+    p.o = static_cast<uint16_t*>(o);
+    p.lse = lse;
+    p.block_table = block_table;
+    p.cu_q = cu_q;
+    p.seq_lens = seq_lens;
+    p.sel = sel;
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_lse = reinterpret_cast<float*>(ws + (size_t)512 * kPagedMaxCtas * d * 4);
+    p.pieces = reinterpret_cast<PagedPiece*>(ws + (size_t)512 * kPagedMaxCtas * (d + 1) * 4);
+    p.B = B;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = G;
+    p.K = K;
+    p.page_shift = shift_of(page_size);
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.causal = causal;
+    p.scale_log2 = scale * kLog2e;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (d == 128)
+        return sel ? launch_paged<128, true>(tq, tk, tv, p, st)
+                   : launch_paged<128, false>(tq, tk, tv, p, st);
+    return sel ? launch_paged<64, true>(tq, tk, tv, p, st)
+               : launch_paged<64, false>(tq, tk, tv, p, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_page_tables(const int* ctx_lens, const int* new_lens, const int* free_pages,
+                               const int* free_head, int* free_head_out, int* block_table,
+                               int* seq_lens, int* cu_q, long long* slot_map, int B, int T,
+                               int num_free, int page_size, int max_pages_per_seq, int num_pages,
+                               void* stream) {
+    if (!ctx_lens || !new_lens || !free_pages || !free_head || !free_head_out || !block_table ||
+        !seq_lens || !cu_q || !slot_map)
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t s = check_pages(B, 1, 64, page_size, max_pages_per_seq, num_pages);
+    if (s != ATTN_OK) return s;
+    if (T < 1 || T > (1 << 30) || num_free < 1) return ATTN_ERR_INVALID_ARG;
+    if (B > kTablesMaxSeqs) return ATTN_ERR_UNSUPPORTED;
+    if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) ||
+        !aligned(free_head, 4) || !aligned(free_head_out, 4) || !aligned(block_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(slot_map, 8))
+        return ATTN_ERR_ALIGNMENT;
+    const int dev = current_device();
+    if (dev < 0 || dev >= 64) return ATTN_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(g_dev_mu);
+        if (!g_dev[dev].tables_attr_set) {
+            if (cudaFuncSetAttribute(attn_page_tables_kernel,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (3 * kTablesMaxSeqs + 1) * 4) != cudaSuccess)
+                return ATTN_ERR_CUDA;
+            g_dev[dev].tables_attr_set = true;
+        }
+    }
+    TablesParams p{ctx_lens, new_lens,  free_pages, free_head, free_head_out,
+                   block_table, seq_lens, cu_q,     slot_map,  B,
+                   T,        num_free,  shift_of(page_size), max_pages_per_seq, num_pages};
+    const int ctas = T <= kTablesThreads ? 1 : T <= 2 * kTablesThreads ? 2 : 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kTablesThreads);
+    cfg.dynamicSmemBytes = (size_t)(3 * B + 1) * 4;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, attn_page_tables_kernel, p) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
+    return ATTN_OK;
+}
+
+attn_status_t attn_paged_append(const void* k, const void* v, const long long* slot_map,
+                                void* k_cache, void* v_cache, void* k_bounds, int T, int Hkv,
+                                int d, long long kv_stride, int page_size, int num_pages,
+                                void* stream) {
+    if (!k || !v || !slot_map || !k_cache || !v_cache) return ATTN_ERR_INVALID_ARG;
+    attn_status_t s = check_pages(1, Hkv, d, page_size, 1, num_pages);
+    if (s != ATTN_OK) return s;
+    if (T < 1 || T > (1 << 30)) return ATTN_ERR_INVALID_ARG;
+    if (kv_stride < (long long)Hkv * d || kv_stride > (1ll << 36)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        (k_bounds && !aligned(k_bounds, 16)) || !aligned(slot_map, 8) || kv_stride % 8 != 0)
+        return ATTN_ERR_ALIGNMENT;
+    AppendParams p;
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.slot_map = slot_map;
+    p.k_cache = static_cast<uint16_t*>(k_cache);
+    p.v_cache = static_cast<uint16_t*>(v_cache);
+    p.bounds = static_cast<uint16_t*>(k_bounds);
+    p.kv_stride = kv_stride;
+    p.num_slots = (long long)num_pages * page_size;
+    p.T = T;
+    p.Hkv = Hkv;
+    p.page_shift = shift_of(page_size);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool many = (long long)T * Hkv >= 32768;
+    const dim3 grid(many ? (T + 31) / 32 : T, Hkv);
+    if (d == 128) {
+        if (many) attn_paged_append_kernel<128, 32><<<grid, kAppendThreads, 0, st>>>(p);
+        else attn_paged_append_kernel<128, 1><<<grid, kAppendThreads, 0, st>>>(p);
+    } else {
+        if (many) attn_paged_append_kernel<64, 32><<<grid, kAppendThreads, 0, st>>>(p);
+        else attn_paged_append_kernel<64, 1><<<grid, kAppendThreads, 0, st>>>(p);
+    }
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_fwd_paged_workspace_bytes(int d) {
+    if (d != 64 && d != 128) return 0;
+    return (size_t)512 * kPagedMaxCtas * (d + 1) * 4 + round256(2 * kPagedMaxCtas * sizeof(PagedPiece));
+}
+
+attn_status_t attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache,
+                             const int* block_table, const int* cu_q, const int* seq_lens, void* o,
+                             float* lse, int B, int T, int Hq, int Hkv, int d, long long q_stride,
+                             int page_size, int max_pages_per_seq, int num_pages, int causal,
+                             float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    return paged_entry(q, k_cache, v_cache, block_table, cu_q, seq_lens, nullptr, 0, o, lse, B, T,
+                       Hq, Hkv, d, q_stride, page_size, max_pages_per_seq, num_pages, causal,
+                       scale, workspace, workspace_bytes, stream);
+}
+
+attn_status_t attn_sparse_paged(const void* q, const void* k_cache, const void* v_cache,
+                                const int* block_table, const int* cu_q, const int* seq_lens,
+                                const int* sel, void* o, float* lse, int B, int T, int Hq, int Hkv,
+                                int d, int num_sel, long long q_stride, int page_size,
+                                int max_pages_per_seq, int num_pages, float scale, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    if (!sel) return ATTN_ERR_INVALID_ARG;
+    return paged_entry(q, k_cache, v_cache, block_table, cu_q, seq_lens, sel, num_sel, o, lse, B,
+                       T, Hq, Hkv, d, q_stride, page_size, max_pages_per_seq, num_pages, 1, scale,
+                       workspace, workspace_bytes, stream);
+}
+
+size_t attn_page_select_workspace_bytes(int T, int Hkv, int max_pages_per_seq) {
+    if (T < 1 || Hkv < 1 || max_pages_per_seq < 1) return 0;
+    return round256((size_t)T * Hkv * max_pages_per_seq * 8);
+}
+
+}  // extern "C"
+
+namespace {
+template <int D>
+attn_status_t launch_select(const SelectParams& p, cudaStream_t st) {
+    const long long rows = (long long)p.T * p.Hkv;
+    const int smem = p.G * D * 8;
+    if (smem > 48 * 1024) {
+        const int dev = current_device();
+        if (dev < 0 || dev >= 64) return ATTN_ERR_CUDA;
+        std::lock_guard<std::mutex> lk(g_dev_mu);
+        bool& set = g_dev[dev].score_attr_set[D == 128 ? 1 : 0];
+        if (!set) {
+            if (cudaFuncSetAttribute(attn_page_score_kernel<D>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     128 * D * 8) != cudaSuccess)
+                return ATTN_ERR_CUDA;
+            set = true;
+        }
+    }
+    const dim3 grid((p.max_pages + kScoreThreads - 1) / kScoreThreads,
+                    (unsigned)(rows < 65535 ? rows : 65535), (unsigned)((rows + 65534) / 65535));
+    attn_page_score_kernel<D><<<grid, kScoreThreads, smem, st>>>(p);
+    // the least registers that hold a row's keys
+    if (p.max_pages <= 32 * 8)
+        attn_page_topk_kernel<32, 8><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p);
+    else if (p.max_pages <= 32 * 32)
+        attn_page_topk_kernel<32, 32><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p);
+    else if (p.max_pages <= 1024 * 4)
+        attn_page_topk_kernel<1024, 4><<<(unsigned)rows, 1024, 0, st>>>(p);
+    else
+        attn_page_topk_kernel<1024, 16><<<(unsigned)rows, 1024, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_page_select(const void* q, const void* k_bounds, const int* block_table,
+                               const int* cu_q, const int* seq_lens, int* sel, int B, int T,
+                               int Hq, int Hkv, int d, int num_sel, int keep_first, int keep_last,
+                               long long q_stride, int page_size, int max_pages_per_seq,
+                               int num_pages, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    if (!q || !k_bounds || !block_table || !cu_q || !seq_lens || !sel || !workspace)
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t s = check_pages(B, Hkv, d, page_size, max_pages_per_seq, num_pages);
+    if (s != ATTN_OK) return s;
+    if (T < 1 || T > (1 << 30) || Hq < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+    if (num_sel < 1 || keep_first < 0 || keep_last < 0 ||
+        (long long)keep_first + keep_last > num_sel)
+        return ATTN_ERR_INVALID_ARG;
+    if (Hq / Hkv > 128 || max_pages_per_seq > 16384) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)T * Hkv > (1ll << 30)) return ATTN_ERR_INVALID_ARG;
+    if (q_stride < (long long)Hq * d || q_stride > (1ll << 36)) return ATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < attn_page_select_workspace_bytes(T, Hkv, max_pages_per_seq))
+        return ATTN_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_bounds, 16) || !aligned(block_table, 4) ||
+        !aligned(cu_q, 4) || !aligned(seq_lens, 4) || !aligned(sel, 4) ||
+        !aligned(workspace, 256) || q_stride % 8 != 0)
+        return ATTN_ERR_ALIGNMENT;
+    SelectParams p;
+    p.q = static_cast<const uint16_t*>(q);
+    p.bounds = static_cast<const uint16_t*>(k_bounds);
+    p.block_table = block_table;
+    p.cu_q = cu_q;
+    p.seq_lens = seq_lens;
+    p.sel = sel;
+    p.keys = static_cast<unsigned long long*>(workspace);
+    p.q_stride = q_stride;
+    p.B = B;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.K = num_sel;
+    p.first = keep_first;
+    p.last = keep_last;
+    p.page_shift = shift_of(page_size);
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return d == 128 ? launch_select<128>(p, st) : launch_select<64>(p, st);
 }
 
 }  // extern "C"

@@ -266,6 +266,153 @@ attn_status_t attn_decode_splitkv_noalloc(const void *q, const void *k, const vo
                                           int num_splits, void *stream);
 
 /*
+ * Serving on a paged K/V cache. A step runs, in this order: attn_page_tables
+ * (pages and slots of the step's tokens), attn_paged_append (their K and V into
+ * the cache) and attn_fwd_paged (their attention), or, over long caches,
+ * attn_page_select and attn_sparse_paged in its place. The pages name "paged
+ * variants for decode" (mantramindai, "Versions", last paragraph; PagedAttention
+ * in appliedaiprep, "What interviewers probe next") and give no layout; these
+ * entry points use attn_decode_paged's caches and tables, with Hkv K/V heads
+ * shared by Hq = G * Hkv query heads (head h reads K/V head h / G):
+ *   k_cache, v_cache  bf16 [num_pages, Hkv, page_size, d]
+ *   block_table       int32 [B, max_pages_per_seq]; entries a sequence does not
+ *                     use yet may hold anything
+ *   cu_q              int32 [B + 1], ascending: the step's rows cu_q[b] ..
+ *                     cu_q[b+1]-1 (of T) are sequence b's new tokens
+ *   seq_lens          int32 [B], tokens cached per sequence, this step's included
+ * so sequence b's i-th new token sits at position seq_lens[b] - n_b + i, with
+ * n_b = cu_q[b+1] - cu_q[b]. Rows at or past cu_q[B] belong to no sequence:
+ * their outputs are left as they were. Lengths, offsets, table entries and page
+ * numbers are checked on the device: what is out of range is clamped or skipped,
+ * never dereferenced, and attn_status() reports ATTN_ERR_BAD_INDEX. Rows of q, k
+ * and v may be any multiple of 8 elements apart (q_stride, kv_stride), so they
+ * may be views of one projection's output. page_size is a power of two in [16, 1024].
+ */
+
+/*
+ * Block tables, lengths, row offsets and slots of one step.
+ *
+ *   ctx_lens      int32 [B]   (read)  tokens each sequence holds before the step
+ *   new_lens      int32 [B]   (read)  tokens it adds (0 or more)
+ *   free_pages    int32 [num_free] (read)  page numbers to hand out, in order
+ *   free_head     int32 [1]   (read)  how many of them are handed out already
+ *   free_head_out int32 [1]   (written) the same after the step; may be free_head
+ *   block_table   (written)   the pages added to a sequence: its logical pages
+ *                 ceil(ctx/page_size) .. ceil((ctx+new)/page_size)-1, taken in
+ *                 order of sequence and page; other entries are left as they were
+ *   seq_lens      int32 [B] (written) ctx + new; may be ctx_lens
+ *   cu_q          int32 [B + 1] (written) exclusive prefix sum of new
+ *   slot_map      int64 [T] (written) page * page_size + offset of every row's
+ *                 token; -1 for rows of no sequence and tokens without a page
+ *   B <= 8192 (ATTN_ERR_UNSUPPORTED); T >= 1 rows; num_free >= 1.
+ *   A sequence whose lengths are negative or exceed its table gets no token
+ *   (seq_lens = ctx clamped to the table); tokens past row T are cut off and do
+ *   not count; a page past the end of the free list or outside [0, num_pages) is
+ *   entered as -1. attn_status() reports ATTN_ERR_BAD_INDEX for each of them.
+ */
+attn_status_t attn_page_tables(const int *ctx_lens, const int *new_lens, const int *free_pages,
+                               const int *free_head, int *free_head_out, int *block_table,
+                               int *seq_lens, int *cu_q, long long *slot_map, int B, int T,
+                               int num_free, int page_size, int max_pages_per_seq, int num_pages,
+                               void *stream);
+
+/*
+ * Writes a step's K and V into the cache, and each written page's key bounds.
+ *
+ *   k, v       bf16 [T, Hkv, d], rows kv_stride elements apart   (read)
+ *   slot_map   int64 [T]   (read) as attn_page_tables makes it; rows with a
+ *              negative slot are skipped, the others must differ
+ *   k_cache, v_cache       (written at those slots)
+ *   k_bounds   bf16 [num_pages, Hkv, 2, d], or NULL (written for every page
+ *              written to): [.., 0, :] the least and [.., 1, :] the largest key of
+ *              each channel over the page's slots up to the last one written; a NaN
+ *              key gives NaN. A page's rows must follow one another in slot_map, in
+ *              ascending order, and its earlier slots must be filled.
+ *   kv_stride >= Hkv * d, a multiple of 8.
+ */
+attn_status_t attn_paged_append(const void *k, const void *v, const long long *slot_map,
+                                void *k_cache, void *v_cache, void *k_bounds, int T, int Hkv,
+                                int d, long long kv_stride, int page_size, int num_pages,
+                                void *stream);
+
+/*
+ * Bytes of device workspace that attn_fwd_paged and attn_sparse_paged need
+ * (partial rows of units that two CTAs share), or 0 if d is invalid. It depends
+ * on d alone. Nothing in it needs initialising; calls that run at the same time
+ * (two captured graphs too) must not share one.
+ */
+size_t attn_fwd_paged_workspace_bytes(int d);
+
+/*
+ * Attention of every sequence's new tokens over its cached keys: chunked
+ * prefill, prefill of whole prompts, verification of drafted tokens and decode,
+ * in one batch of ragged rows. O and LSE as attn_fwd defines them, in the
+ * tiles-and-online-softmax form of mantramindai, "The two ideas"; long key
+ * sequences are split across CTAs and merged as in the same page's "Follow-up
+ * questions to expect", last question.
+ *
+ *   q    bf16 [T, Hq, d], rows q_stride elements apart   (read)
+ *   o    bf16 [T, Hq, d]   (written)
+ *   lse  fp32 [T, Hq]      (written; natural log)
+ *   causal 1: a token sees the keys up to its own position; 0: all seq_lens[b]
+ *   keys. A row that sees no key gets O = 0, LSE = -inf.
+ *   d in {64, 128}; Hq a multiple of Hkv with Hq / Hkv <= 128; T >= 1 rows;
+ *   workspace 256-byte aligned, attn_fwd_paged_workspace_bytes(d) bytes.
+ *   What a page holds past the sequence's last token never matters. Keys that
+ *   cannot be read (bad table entries) are skipped. V of the cached tokens
+ *   must be finite: a tile's product takes in the tokens that the causal mask hides from a row.
+ */
+attn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache,
+                             const int *block_table, const int *cu_q, const int *seq_lens, void *o,
+                             float *lse, int B, int T, int Hq, int Hkv, int d, long long q_stride,
+                             int page_size, int max_pages_per_seq, int num_pages, int causal,
+                             float scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Bytes of device workspace attn_page_select needs, or 0 for invalid sizes.
+ */
+size_t attn_page_select_workspace_bytes(int T, int Hkv, int max_pages_per_seq);
+
+/*
+ * The pages each new token reads, by an upper bound of its scores: with bounds
+ * lo, hi of a page's keys (attn_paged_append), q . k <= sum_c (q_c >= 0 ? q_c
+ * hi_c : q_c lo_c), and a page's score for a K/V head is the largest of these
+ * over the group's query heads. A token at position pos sees pages
+ * 0 .. pos / page_size. Of these it gets the first keep_first, the last
+ * keep_last and those with the highest scores, num_sel in all (the lowest page first among
+ * equal scores); fewer if it sees fewer.
+ *
+ *   k_bounds  bf16 [num_pages, Hkv, 2, d] (read; finite: a page whose score is
+ *             NaN ranks above all others)
+ *   sel       int32 [T, Hkv, num_sel] (written): logical pages, ascending, then -1
+ *   num_sel >= 1, keep_first + keep_last <= num_sel, max_pages_per_seq <= 16384,
+ *   Hq / Hkv <= 128 (ATTN_ERR_UNSUPPORTED beyond). Sums are taken in 64 bits.
+ */
+attn_status_t attn_page_select(const void *q, const void *k_bounds, const int *block_table,
+                               const int *cu_q, const int *seq_lens, int *sel, int B, int T,
+                               int Hq, int Hkv, int d, int num_sel, int keep_first, int keep_last,
+                               long long q_stride, int page_size, int max_pages_per_seq,
+                               int num_pages, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * Attention of every new token over the tokens of the pages listed for it and
+ * its K/V head, up to its own position: attn_fwd_paged (causal) with the other
+ * pages left out. Arguments as there, and
+ *   sel  int32 [T, Hkv, num_sel]  (read): logical pages in any order; -1 is
+ *        skipped, pages past the token's position hold no visible key, entries
+ *        past the sequence's last page are skipped and reported. A page listed
+ *        twice counts twice.
+ *   num_sel >= 1, num_sel * max(1, page_size / 128) <= 1024.
+ */
+attn_status_t attn_sparse_paged(const void *q, const void *k_cache, const void *v_cache,
+                                const int *block_table, const int *cu_q, const int *seq_lens,
+                                const int *sel, void *o, float *lse, int B, int T, int Hq, int Hkv,
+                                int d, int num_sel, long long q_stride, int page_size,
+                                int max_pages_per_seq, int num_pages, float scale, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
  * Backward pass: bytes of device workspace attn_bwd needs, or 0 if the
  * arguments are invalid. Layout (owned by the caller, 256-byte aligned), with
  * NqPad = Nq rounded up to a multiple of 64: fp32 D [B, H, NqPad] and fp32
