@@ -28,6 +28,7 @@ __device__ unsigned g_attn_status = 0;
 #include "fwd_sm100.cuh"
 #include "paged_cache_sm100.cuh"
 #include "paged_fwd_sm100.cuh"
+#include "paged_rows_sm100.cuh"
 
 using namespace eattn;
 
@@ -128,7 +129,7 @@ bool encode_q_map(CUtensorMap* map, const void* base, int T, int Hq, int D, long
 
 struct DeviceInfo {
     int sms = 0;
-    bool paged_attr_set[4] = {false, false, false, false};
+    bool paged_attr_set[16] = {};
     bool tables_attr_set = false;
     bool score_attr_set[2] = {false, false};
     bool fwd_attr_set[8] = {false, false, false, false, false, false, false, false};
@@ -687,13 +688,16 @@ int shift_of(int page_size) {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <int D, bool SPARSE>
+// N = 0: 128-row tiles; else at most N rows per unit
+template <int D, int N, bool SPARSE>
 attn_status_t launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const PagedParams& p, cudaStream_t stream) {
-    using T = PagedTraits<D>;
+    using T = PagedTraits<D, N>;
     const int dev = current_device();
     if (dev < 0 || dev >= 64) return ATTN_ERR_CUDA;
-    auto kern = attn_paged_sm100_kernel<D, SPARSE>;
+    void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, PagedParams);
+    if constexpr (N == 0) kern = attn_paged_sm100_kernel<D, SPARSE>;
+    else kern = attn_paged_rows_sm100_kernel<D, N, SPARSE>;
     int sms;
     {
         std::lock_guard<std::mutex> lk(g_dev_mu);
@@ -701,7 +705,8 @@ attn_status_t launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const C
         if (di.sms == 0 &&
             cudaDeviceGetAttribute(&di.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return ATTN_ERR_CUDA;
-        const int slot = (SPARSE ? 2 : 0) + (D == 128 ? 1 : 0);
+        const int slot = (N == 16 ? 4 : N == 32 ? 8 : N == 64 ? 12 : 0) + (SPARSE ? 2 : 0) +
+                         (D == 128 ? 1 : 0);
         if (!di.paged_attr_set[slot]) {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      T::kSmemBytes) != cudaSuccess)
@@ -712,9 +717,21 @@ attn_status_t launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const C
     }
     const int grid = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
     kern<<<grid, kPagedThreads, T::kSmemBytes, stream>>>(tq, tk, tv, p);
-    attn_paged_merge_kernel<D><<<dim3(grid, 256 * D / 4 / kPagedMergeThreads), kPagedMergeThreads,
-                                 0, stream>>>(p, grid);
+    constexpr int kUnitRows = N ? N : 256;
+    attn_paged_merge_kernel<D><<<dim3(grid, kUnitRows * D / 4 / kPagedMergeThreads),
+                                 kPagedMergeThreads, 0, stream>>>(p, grid);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <int D, bool SPARSE>
+attn_status_t launch_paged_rows(int rows, const CUtensorMap& tq, const CUtensorMap& tk,
+                                const CUtensorMap& tv, const PagedParams& p, cudaStream_t st) {
+    switch (rows) {
+        case 16: return launch_paged<D, 16, SPARSE>(tq, tk, tv, p, st);
+        case 32: return launch_paged<D, 32, SPARSE>(tq, tk, tv, p, st);
+        case 64: return launch_paged<D, 64, SPARSE>(tq, tk, tv, p, st);
+    }
+    return launch_paged<D, 0, SPARSE>(tq, tk, tv, p, st);
 }
 
 // attn_fwd_paged, and attn_sparse_paged (sel not null)
@@ -748,7 +765,12 @@ attn_status_t paged_entry(const void* q, const void* k_cache, const void* v_cach
         return ATTN_ERR_ALIGNMENT;
 
     PagedParams p;
-    p.tpt = sel ? 1 : 128 / G;
+    // Rows of a unit: with few tokens per sequence (on average; the lengths are on the
+    // device) the turned kernel, whose work follows the rows in use, else 128-row tiles.
+    const long long avg = sel ? 1 : (T + (long long)B - 1) / B;
+    const int rows = avg * G <= 16 ? 16 : avg * G <= 32 ? 32 : avg * G <= 64 ? 64 : 0;
+    p.tpt = sel ? 1 : (rows ? rows : 128) / G;
+    p.unit_tok = sel || rows ? p.tpt : 2 * p.tpt;
     const int box = page_size < 128 ? page_size : 128;
     CUtensorMap tq, tk, tv;
     if (!encode_q_map(&tq, q, T, Hq, d, q_stride, G, p.tpt) ||
@@ -778,10 +800,10 @@ attn_status_t paged_entry(const void* q, const void* k_cache, const void* v_cach
     p.scale_log2 = scale * kLog2e;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (d == 128)
-        return sel ? launch_paged<128, true>(tq, tk, tv, p, st)
-                   : launch_paged<128, false>(tq, tk, tv, p, st);
-    return sel ? launch_paged<64, true>(tq, tk, tv, p, st)
-               : launch_paged<64, false>(tq, tk, tv, p, st);
+        return sel ? launch_paged_rows<128, true>(rows, tq, tk, tv, p, st)
+                   : launch_paged_rows<128, false>(rows, tq, tk, tv, p, st);
+    return sel ? launch_paged_rows<64, true>(rows, tq, tk, tv, p, st)
+               : launch_paged_rows<64, false>(rows, tq, tk, tv, p, st);
 }
 
 }  // namespace

@@ -69,28 +69,39 @@ struct PagedParams {
     float* part_lse;          // fp32 [2 * kPagedMaxCtas][256]
     PagedPiece* pieces;       // [2 * kPagedMaxCtas]
     int B, T, Hq, Hkv, G, K;
-    int tpt;                  // tokens of a Q tile
+    int tpt, unit_tok;        // tokens of a Q tile and of a unit
     int page_shift, max_pages, num_pages;
     int causal;
     float scale_log2;
 };
 
-template <int D>
+// N = 0: 128-row Q tiles (this file); N = 16, 32, 64: at most N rows per unit, kept as columns
+// (paged_rows_sm100.cuh).
+template <int D, int N = 0>
 struct PagedTraits {
+    static constexpr int kD = D, kN = N;
     static constexpr int kPanels = D / 64;
     static constexpr int kPanelBytes = 128 * 128;
     static constexpr int kTileBytes = kPanels * kPanelBytes;
-    static constexpr int kPairs = D == 128 ? 2 : 4;      // K/V tile pairs in the ring
+    // K/V tile pairs in the ring: what shared memory leaves
+    static constexpr int kPairs = D == 128 ? (N == 16 ? 3 : 2) : N == 16 ? 6 : N == 32 ? 5 : 4;
     static constexpr int kSlots = 2 * kPairs;
     static constexpr int kUnits = 4;                     // unit records in flight
     static constexpr int kMasks = 2 * kPairs;
+    static constexpr int kQRows = N ? N : 128;
+    static constexpr int kQPanelBytes = kQRows * 128;
+    static constexpr int kQBytes = kPanels * kQPanelBytes;    // one Q slot (of two)
+    static constexpr int kIssuers = N ? 2 : 1;           // threads that issue products
     static constexpr int kStageWarpBytes = 32 * 64;
-    static constexpr int kStageBytes = 8 * kStageWarpBytes;
-    static constexpr int kBars = 2 * kSlots + kPairs + 4 + 4 + 8 + 2 * kUnits + 2 + kMasks;
-    static constexpr int kOffStage = (2 + kSlots) * kTileBytes;
+    // N = 0: the epilogue's staging blocks; else P of both softmax groups (N x 128 bf16 each)
+    static constexpr int kStageBytes = N ? 2 * N * 256 : 8 * kStageWarpBytes;
+    static constexpr int kMlBytes = N ? 2 * N * 8 + 2 * 6 * N * 4 : 128 * 8;
+    static constexpr int kBars = 2 * kSlots + kPairs + 4 + 4 + 8 + 2 * kUnits + 2 + 2 * kMasks;
+    static constexpr int kOffKV = 2 * kQBytes;
+    static constexpr int kOffStage = kOffKV + kSlots * kTileBytes;
     static constexpr int kOffList = kOffStage + kStageBytes;
     static constexpr int kOffMl = kOffList + kPagedListMax * 8;
-    static constexpr int kOffMask = kOffMl + 128 * 8;
+    static constexpr int kOffMask = kOffMl + kMlBytes;
     static constexpr int kOffUnits = kOffMask + kMasks * 16;
     static constexpr int kOffBars = kOffUnits + kUnits * 64;
     static constexpr int kOffMisc = kOffBars + kBars * 8;
@@ -101,12 +112,12 @@ struct PagedTraits {
     static constexpr int kLaunchRegs = 168, kSoftmaxRegs = 192, kOtherRegs = 120;
     static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kPagedThreads * kLaunchRegs,
                   "register split exceeds the launch allocation");
-    static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 384;
+    static constexpr uint32_t kColS0 = 0, kColS1 = N ? 64 : 128, kColO0 = N ? 128 : 256,
+                              kColO1 = N ? 192 : 384;
 };
 
-template <int D>
+template <class T>
 struct PagedBars {
-    using T = PagedTraits<D>;
     uint32_t base;
     __device__ __forceinline__ uint32_t at(int i) const { return base + 8 * i; }
     __device__ __forceinline__ uint32_t kv_full(int i) const { return at(i); }
@@ -127,8 +138,15 @@ struct PagedBars {
     }
     __device__ __forceinline__ uint32_t ml_full() const { return at(kA + 16 + 2 * T::kUnits); }
     __device__ __forceinline__ uint32_t drain() const { return at(kA + 17 + 2 * T::kUnits); }
+    // Key tile x of the CTA: its mask is written and its K slot has been given to it
+    // (entry x % kMasks), and the same for its V slot. A parity tells only the
+    // last two uses of a slot apart, so a thread that has not itself waited for the
+    // slot's previous use waits for these first.
     __device__ __forceinline__ uint32_t mask_full(int i) const {
         return at(kA + 18 + 2 * T::kUnits + i);
+    }
+    __device__ __forceinline__ uint32_t v_given(int i) const {
+        return at(kA + 18 + 2 * T::kUnits + T::kMasks + i);
     }
 };
 
@@ -171,7 +189,7 @@ struct PagedLine {
     long long base;
     int U, n, m, slope;
     __device__ __forceinline__ PagedLine(const PagedParams& p, const PagedSeq& s) {
-        U = p.sel ? 1 : 2 * p.tpt;
+        U = p.unit_tok;
         n = s.n;
         m = (s.n + U - 1) / U;
         slope = (!p.sel && p.causal) ? 1 : 0;
@@ -285,12 +303,11 @@ __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap
 }
 
 // The producer warp, all lanes together.
-template <int D, bool SPARSE>
+template <class T, bool SPARSE>
 __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, const CUtensorMap* tq,
                                const CUtensorMap* tk, const CUtensorMap* tv,
-                               const PagedBars<D>& b, const PagedShared& sh, int lane) {
-    using T = PagedTraits<D>;
-    const uint32_t sQ = smem_addr(sh.smem), sKV = sQ + 2 * T::kTileBytes;
+                               const PagedBars<T>& b, const PagedShared& sh, int lane) {
+    const uint32_t sQ = smem_addr(sh.smem), sKV = sQ + T::kOffKV;
     PagedUnit* ring = reinterpret_cast<PagedUnit*>(sh.smem + T::kOffUnits);
     int2* list = reinterpret_cast<int2*>(sh.smem + T::kOffList);
     volatile int* abort_flag = sh.abort_flag;
@@ -448,7 +465,7 @@ __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, con
                         mbar_arrive_expect_tx(b.q_full(slot),
                                               (uint32_t)(T::kPanels * p.tpt * p.G * 128));
                         for (int pn = 0; pn < T::kPanels; ++pn)
-                            tma_load_3d(sQ + slot * T::kTileBytes + pn * T::kPanelBytes, tq,
+                            tma_load_3d(sQ + slot * T::kQBytes + pn * T::kQPanelBytes, tq,
                                         b.q_full(slot), pn * 64, hk * p.G, u.tok + t * p.tpt);
                     }
                     ++q_used[slot];
@@ -501,8 +518,8 @@ __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, con
                             sh.smem + T::kOffMask)[(it % T::kMasks) * 4 + lane] = word;
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(b.mask_full(it % T::kMasks));
                         mbar_arrive_expect_tx(b.kv_full(sk), T::kTileBytes);
+                        mbar_arrive(b.mask_full(it % T::kMasks));
                     }
                     __syncwarp();
                     if (issues)
@@ -536,6 +553,7 @@ __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, con
                         if (lane == 0) mbar_arrive_expect_tx(vbar, T::kTileBytes);
                         raw_last &= ~(1u << pair);
                     }
+                    if (T::kIssuers > 1 && lane == 0) mbar_arrive(b.v_given(it % T::kMasks));
                     __syncwarp();
                     if (issues)
                         tma_load_3d_hint(sKV + sv * T::kTileBytes + box_off, tv, vbar, panel * 64,
@@ -599,10 +617,9 @@ fail:
 }
 
 // Zeroes the V rows of keys that do not exist (a whole warp).
-template <int D>
-__device__ void paged_tail(const PagedBars<D>& b, const PagedShared& sh, int lane) {
-    using T = PagedTraits<D>;
-    const uint32_t sKV = smem_addr(sh.smem) + 2 * T::kTileBytes;
+template <class T>
+__device__ void paged_tail(const PagedBars<T>& b, const PagedShared& sh, int lane) {
+    const uint32_t sKV = smem_addr(sh.smem) + T::kOffKV;
     uint32_t par = 0;
     for (uint32_t i = 0;; ++i) {
         if (!warp_wait(b.tail_full(i & 1), (i >> 1) & 1, sh.abort_flag)) return;
@@ -635,12 +652,13 @@ __device__ void paged_tail(const PagedBars<D>& b, const PagedShared& sh, int lan
 // S_t(i + 1), which overwrites P_t(i). A wide unit's step i uses key tile i for
 // both t, a narrow one's key tile 2 i + t.
 template <int D>
-__device__ void paged_mma(uint32_t tbase, const PagedBars<D>& b, const PagedShared& sh) {
+__device__ void paged_mma(uint32_t tbase, const PagedBars<PagedTraits<D>>& b,
+                          const PagedShared& sh) {
     using T = PagedTraits<D>;
     using F = FwdTraits<D, false>;
     static_assert(F::kTileBytes == T::kTileBytes && F::kPanelBytes == T::kPanelBytes, "tiles");
     constexpr uint64_t kTileStep = T::kTileBytes >> 4;
-    const uint32_t sQ = smem_addr(sh.smem), sKV = sQ + 2 * T::kTileBytes;
+    const uint32_t sQ = smem_addr(sh.smem), sKV = sQ + T::kOffKV;
     const uint64_t dq0 = fwd_sdesc<F>(sQ, 16);
     const uint64_t dk0 = fwd_sdesc<F>(sKV, 16);
     const uint64_t dv0 = fwd_sdesc<F>(sKV, T::kPanelBytes);
@@ -745,8 +763,9 @@ __device__ __forceinline__ void paged_store_chunk(uint32_t stage, const uint32_t
 }
 
 template <int D>
-__device__ void paged_softmax(const PagedParams& p, uint32_t tbase, const PagedBars<D>& b,
-                              const PagedShared& sh, int warp, int lane) {
+__device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
+                              const PagedBars<PagedTraits<D>>& b, const PagedShared& sh, int warp,
+                              int lane) {
     using T = PagedTraits<D>;
     const int t = warp >> 2;                 // Q tile, or softmax group of a narrow unit
     const int quarter = warp & 3;            // tensor-memory lanes this warp may access
@@ -892,8 +911,9 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase, const PagedB
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b.ml_full());
             } else {
-                if (!warp_wait(b.o_final(1), o_used[1] & 1, abort_flag)) return;
+                // group 1 has waited for its own o_final by then
                 if (!warp_wait(b.ml_full(), ml_cnt & 1, abort_flag)) return;
+                if (!warp_wait(b.o_final(1), o_used[1] & 1, abort_flag)) return;
                 const float m1 = ml[r].x, l1 = ml[r].y;
                 const float m = fmaxf(m_ref, m1);
                 const float mb = m == -INFINITY ? 0.f : m;
@@ -989,6 +1009,38 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase, const PagedB
 }
 
 // ---------------------------------------------------------------- kernel --
+// One thread initialises the barriers of a CTA.
+template <class T>
+__device__ __forceinline__ void paged_init(const PagedBars<T>& b, const PagedShared& sh) {
+    for (int i = 0; i < T::kSlots; ++i) {
+        mbar_init(b.kv_full(i), 1);
+        mbar_init(b.kv_empty(i), 1);
+    }
+    for (int i = 0; i < T::kPairs; ++i) mbar_init(b.v_raw(i), 1);
+    for (int i = 0; i < T::kMasks; ++i) {
+        mbar_init(b.mask_full(i), 1);
+        mbar_init(b.v_given(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(b.tail_full(i), 1);
+        mbar_init(b.tail_empty(i), 1);
+        mbar_init(b.q_full(i), 1);
+        mbar_init(b.q_empty(i), T::kIssuers);
+        mbar_init(b.s_full(i), 1);
+        mbar_init(b.p_full(i), 4);
+        mbar_init(b.o_final(i), 1);
+        mbar_init(b.o_free(i), 4);
+    }
+    for (int i = 0; i < T::kUnits; ++i) {
+        mbar_init(b.unit_full(i), 1);
+        mbar_init(b.unit_empty(i), T::kIssuers + 8);   // the issuers and 8 softmax warps
+    }
+    mbar_init(b.ml_full(), 4);
+    mbar_init(b.drain(), T::kIssuers);
+    *sh.abort_flag = 0;
+    fence_mbar_init();
+}
+
 template <int D, bool SPARSE>
 __global__ void __launch_bounds__(kPagedThreads, 1)
     attn_paged_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -998,7 +1050,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    PagedBars<D> b;
+    PagedBars<T> b;
     b.base = smem_addr(smem + T::kOffBars);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + T::kOffMisc);
     PagedShared sh;
@@ -1007,32 +1059,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     sh.tail_info = reinterpret_cast<int*>(tmem_holder + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < T::kSlots; ++i) {
-            mbar_init(b.kv_full(i), 1);
-            mbar_init(b.kv_empty(i), 1);
-        }
-        for (int i = 0; i < T::kPairs; ++i) mbar_init(b.v_raw(i), 1);
-        for (int i = 0; i < T::kMasks; ++i) mbar_init(b.mask_full(i), 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(b.tail_full(i), 1);
-            mbar_init(b.tail_empty(i), 1);
-            mbar_init(b.q_full(i), 1);
-            mbar_init(b.q_empty(i), 1);
-            mbar_init(b.s_full(i), 1);
-            mbar_init(b.p_full(i), 4);
-            mbar_init(b.o_final(i), 1);
-            mbar_init(b.o_free(i), 4);
-        }
-        for (int i = 0; i < T::kUnits; ++i) {
-            mbar_init(b.unit_full(i), 1);
-            mbar_init(b.unit_empty(i), 9);   // the MMA thread and 8 softmax warps
-        }
-        mbar_init(b.ml_full(), 4);
-        mbar_init(b.drain(), 1);
-        *sh.abort_flag = 0;
-        fence_mbar_init();
-    }
+    if (threadIdx.x == 0) paged_init<T>(b, sh);
     if (warp == 8 && lane == 0) {
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
@@ -1055,11 +1082,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     } else {
         regs_decrease<T::kOtherRegs>();
         if (warp == 8)
-            paged_producer<D, SPARSE>(p, st, &tm_q, &tm_k, &tm_v, b, sh, lane);
+            paged_producer<T, SPARSE>(p, st, &tm_q, &tm_k, &tm_v, b, sh, lane);
         else if (warp == 9) {
             if (lane == 0) paged_mma<D>(tbase, b, sh);
         } else if (warp == 10)
-            paged_tail<D>(b, sh, lane);
+            paged_tail<T>(b, sh, lane);
     }
     __syncwarp();
     tc_fence_before_sync();

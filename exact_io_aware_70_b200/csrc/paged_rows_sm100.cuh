@@ -1,0 +1,470 @@
+// paged_rows_sm100.cuh -- attention of few rows over a paged K/V cache: decode,
+// drafted tokens, and rows that each read pages of their own.
+//
+// The same sums as paged_fwd_sm100.cuh, for units of at most N = 16, 32 or 64
+// rows (token, head of the group). There, 128 rows of a tile are computed
+// whatever the unit has, and the thread of a row takes its 128 scores one after
+// another: with 4 rows of 128 in use that thread sets the pace (1.4 us per key
+// tile), not memory. Here the tile is turned: keys are the 128 rows of the
+// product and the unit's rows its columns,
+//   S^T = K Q^T  [128 keys x N],   O^T += V^T P^T  [D x N],
+// so 128 threads share each tile's exponentials (N each) and the products take
+// N / 128 of the time. What the turn asks for:
+//   * maxima run across threads. The reference maximum of a row moves only
+//     when a score exceeds it by 2^8 (rare after a unit's first tile), so per
+//     tile the four warps of a group only vote (one barrier with an "or"); the
+//     reduction and the rescaling of O happen when the vote says so.
+//   * sums stay one partial per thread until the unit ends.
+//   * P goes to shared memory (bf16, 128-byte swizzle) as the second operand;
+//     V, stored [keys][D], is the first operand as it lies (M-major).
+// The two softmax groups take alternate key tiles, each with its own issuing
+// thread, so neither waits for the other; group 0 joins the results.
+#pragma once
+
+#include "paged_fwd_sm100.cuh"
+
+namespace eattn {
+
+// Named barrier over one softmax group (ids 1 and 2), and the same with an "or".
+__device__ __forceinline__ void group_sync(int t) {
+    asm volatile("bar.sync %0, 128;" ::"r"(t + 1) : "memory");
+}
+__device__ __forceinline__ bool group_any(int t, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(t + 1)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+
+// N consecutive columns of this warp's 32 tensor-memory lanes
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+    if constexpr (N == 16) {
+        tmem_ld16(taddr, r);
+        tmem_wait_ld16(r);
+    } else if constexpr (N == 32) {
+        tmem_ld32(taddr, r);
+        tmem_wait_ld(r);
+    } else {
+        tmem_ld64(taddr, r);
+        tmem_wait_ld64(r);
+    }
+}
+// ------------------------------------------------------------ MMA issuer --
+// The thread of group t issues S^T and O^T of key tiles t, t + 2, ... of a unit:
+// P(i) V, then S(i + 1). A completed S(i + 1) therefore means that P(i) V is
+// complete too.
+template <int D, int N>
+__device__ void rows_mma(uint32_t tbase, const PagedBars<PagedTraits<D, N>>& b,
+                         const PagedShared& sh, int t) {
+    using T = PagedTraits<D, N>;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, N, false);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(D, N, false) | (1u << 15);   // V^T: M-major
+    const uint32_t sQ = smem_addr(sh.smem), sKV = sQ + T::kOffKV;
+    const uint64_t dq0 = sdesc_sw128(sQ, 16, 1024);
+    const uint64_t dk0 = sdesc_sw128(sKV, 16, 1024);
+    const uint64_t dv0 = sdesc_sw128(sKV, T::kPanelBytes, 1024);
+    const uint64_t dp = sdesc_sw128(sQ + T::kOffStage + t * N * 256, 16, 1024);
+    const uint32_t tS = tbase + (t ? T::kColS1 : T::kColS0);
+    const uint32_t tO = tbase + (t ? T::kColO1 : T::kColO0);
+    volatile int* abort_flag = sh.abort_flag;
+    const PagedUnit* ring = reinterpret_cast<const PagedUnit*>(sh.smem + T::kOffUnits);
+    uint32_t it = 0, units = 0, o_used = 0, p_cnt = 0;
+    uint32_t q_par[2] = {0, 0};
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return mbar_wait(bar, parity, abort_flag, &g_attn_status);
+    };
+    for (;; ++units) {
+        const int ri = units % T::kUnits;
+        if (!wait(b.unit_full(ri), (units / T::kUnits) & 1)) goto done;
+        const volatile PagedUnit& u = ring[ri];
+        const int kind = u.kind, n = t ? u.n1 : u.n0, all = u.n0 + u.n1, qs = u.qs;
+        mbar_arrive(b.unit_empty(ri));
+        if (kind == 0) break;
+        if (all == 0) continue;
+        if (!wait(b.q_full(qs), q_par[qs])) goto done;
+        q_par[qs] ^= 1;
+        const uint64_t dq = dq0 + qs * (T::kQBytes >> 4);
+        auto issue_s = [&](int i) -> bool {
+            const uint32_t x = it + 2 * i + t, sk = 2 * (x % T::kPairs);
+            // the slot's last use may have been the other group's: first see that it is over
+            if (!wait(b.mask_full(x % T::kMasks), (x / T::kMasks) & 1)) return false;
+            if (!wait(b.kv_full(sk), (x / T::kPairs) & 1)) return false;
+            tc_fence_after_sync();
+            const uint64_t dk = dk0 + sk * (T::kTileBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                mma_bf16_ss(tS, dk + (((kk / 4) * T::kPanelBytes + (kk % 4) * 32) >> 4),
+                            dq + (((kk / 4) * T::kQPanelBytes + (kk % 4) * 32) >> 4), idesc_s,
+                            kk > 0 ? 1u : 0u);
+            mma_commit(b.s_full(t));
+            mma_commit(b.kv_empty(sk));
+            if (i == n - 1) mma_commit(b.q_empty(qs));
+            return true;
+        };
+        if (n == 0) {
+            mma_commit(b.q_empty(qs));
+        } else if (!issue_s(0)) {
+            goto done;
+        }
+        for (int i = 0; i < n; ++i) {
+            const uint32_t x = it + 2 * i + t, sv = 2 * (x % T::kPairs) + 1;
+            if (!wait(b.v_given(x % T::kMasks), (x / T::kMasks) & 1)) goto done;
+            if (!wait(b.kv_full(sv), (x / T::kPairs) & 1)) goto done;
+            if (!wait(b.p_full(t), p_cnt & 1)) goto done;
+            ++p_cnt;
+            if (i == 0 && o_used > 0 && !wait(b.o_free(t), (o_used - 1) & 1)) goto done;
+            tc_fence_after_sync();
+            const uint64_t dv = dv0 + sv * (T::kTileBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)      // 16 keys each
+                mma_bf16_ss(tO, dv + ((kk * 16 * 128) >> 4),
+                            dp + (((kk / 4) * N * 128 + (kk % 4) * 32) >> 4), idesc_o,
+                            (i > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(b.kv_empty(sv));
+            if (i == n - 1) mma_commit(b.o_final(t));
+            if (i + 1 < n && !issue_s(i + 1)) goto done;
+        }
+        if (n > 0) ++o_used;
+        it += all;
+    }
+done: {
+    // Every MMA this thread issued must finish before tensor memory is released.
+    volatile int no_abort = 0;
+    mma_commit(b.drain());
+    mbar_wait(b.drain(), 0, &no_abort, &g_attn_status);
+}
+}
+
+// --------------------------------------------------------------- softmax --
+// Thread r of group t is key r of the group's tiles, and then lane r of O^T:
+// dimension r (D = 128), or dimension 16 (r / 32) + r % 32 for r % 32 < 16 (D = 64,
+// a product of 64 rows fills half of each 32 lanes).
+//
+// The four warps of a group meet at named barriers, which wait without a limit: so a
+// warp whose bounded wait has given up goes on to the next vote, and the whole
+// group leaves there together.
+template <int D, int N>
+__device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
+                             const PagedBars<PagedTraits<D, N>>& b, const PagedShared& sh, int warp,
+                             int lane) {
+    using T = PagedTraits<D, N>;
+    const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_off = uint32_t(quarter * 32) << 16;
+    const uint32_t tS = tbase + lane_off + (t ? T::kColS1 : T::kColS0);
+    const uint32_t tO = tbase + lane_off + (t ? T::kColO1 : T::kColO0);
+    const uint32_t tO1 = tbase + lane_off + T::kColO1;
+    volatile int* abort_flag = sh.abort_flag;
+    const PagedUnit* ring = reinterpret_cast<const PagedUnit*>(sh.smem + T::kOffUnits);
+    const volatile uint32_t* masks =
+        reinterpret_cast<const volatile uint32_t*>(sh.smem + T::kOffMask);
+    // per row: group 1's (m, l) and group 0's weights (apart: group 1 may be a unit ahead);
+    // per group: the reference maximum, the factor of a rescaling, a word per warp for reductions
+    float2* ml = reinterpret_cast<float2*>(sh.smem + T::kOffMl);
+    float2* weight = ml + N;
+    float* mref = reinterpret_cast<float*>(sh.smem + T::kOffMl + 2 * N * 8) + t * 6 * N;
+    float* alpha = mref + N;
+    float* red = alpha + N;
+    // where key r of row c goes in P: 128-byte rows of 64 keys, 16-byte pieces swizzled by row
+    const uint32_t sP = smem_addr(sh.smem) + T::kOffStage + t * N * 256 + (r >> 6) * N * 128;
+    const uint32_t piece = (r & 63) >> 3, in_piece = (r & 7) * 2;
+    const float c2 = p.scale_log2;
+    uint32_t it = 0, s_cnt = 0, ml_cnt = 0;
+    uint32_t o_used[2] = {0, 0};
+
+    for (uint32_t units = 0;; ++units) {
+        const int ri = units % T::kUnits;
+        const bool got = warp_wait(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag);
+        if (r < N) mref[r] = -INFINITY;
+        if (group_any(t, !got)) return;
+        const volatile PagedUnit& uu = ring[ri];
+        const int kind = uu.kind, hk = uu.hk, tok0 = uu.tok, ntok = uu.ntok, pos0 = uu.pos0;
+        const int len = uu.len, key0 = uu.key0, un[2] = {uu.n0, uu.n1}, slot = uu.slot;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.unit_empty(ri));
+        if (kind == 0) break;
+        const int n = un[t], rows = ntok * p.G;   // columns [0, rows) are in use
+        const bool diag = p.causal && len != 0x7fffffff;
+        float l[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) l[c] = 0.f;
+        for (int i = 0; i < n; ++i) {
+            const uint32_t x = it + 2 * i + t;
+            bool ok = warp_wait(b.mask_full(x % T::kMasks), (x / T::kMasks) & 1, abort_flag);
+            const bool there = (masks[4 * (x % T::kMasks) + quarter] >> lane) & 1;
+            // rows [first, N) see this key
+            const long long key = (long long)key0 + (2 * i + t) * 128 + r;
+            const long long behind = diag ? key - pos0 : 0;   // tokens before the key's own
+            const int first = !there ? N : behind <= 0 ? 0 : behind >= N ? N : (int)behind * p.G;
+            ok = ok && warp_wait(b.s_full(t), s_cnt & 1, abort_flag);
+            ++s_cnt;
+            tc_fence_after_sync();
+            uint32_t sr[N];
+            tmem_ld_cols<N>(tS, sr);
+            // the score of column c in log2 units
+            auto score = [&](int c) { return c >= first ? __uint_as_float(sr[c]) * c2 : -INFINITY; };
+            bool over = !ok;
+#pragma unroll
+            for (int c4 = 0; c4 < N; c4 += 4) {
+                if (c4 < rows) {
+                    const float4 m = *reinterpret_cast<const float4*>(mref + c4);
+                    const float mm[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) over |= score(c4 + k) > mm[k] + 8.0f;
+                }
+            }
+            if (group_any(t, over)) {
+                if (group_any(t, !ok)) return;
+                // the reference of every row moves to its maximum so far
+#pragma unroll
+                for (int c4 = 0; c4 < N; c4 += 4) {
+                    if (c4 < rows) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float v = score(c4 + k);
+#pragma unroll
+                            for (int off = 16; off > 0; off >>= 1)
+                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                            if (lane == 0) red[quarter * N + c4 + k] = v;
+                        }
+                    }
+                }
+                group_sync(t);
+                if (r < N && r < rows) {
+                    const float m_old = mref[r];
+                    const float v = fmaxf(fmaxf(red[r], red[N + r]),
+                                          fmaxf(red[2 * N + r], red[3 * N + r]));
+                    const float m_new = fmaxf(m_old, v);
+                    alpha[r] = m_new == -INFINITY ? 1.0f : fast_exp2(m_old - m_new);
+                    mref[r] = m_new;
+                }
+                group_sync(t);
+#pragma unroll
+                for (int c4 = 0; c4 < N; c4 += 4) {
+                    if (c4 < rows) {
+                        const float4 a = *reinterpret_cast<const float4*>(alpha + c4);
+                        l[c4] *= a.x;
+                        l[c4 + 1] *= a.y;
+                        l[c4 + 2] *= a.z;
+                        l[c4 + 3] *= a.w;
+                    }
+                }
+                if (i > 0) {      // S(i) is complete, so P(i-1) V is
+#pragma unroll 1
+                    for (int c = 0; c < rows; c += 16) {
+                        uint32_t orr[16];
+                        tmem_ld16(tO + c, orr);
+                        tmem_wait_ld16(orr);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            orr[k] = __float_as_uint(__uint_as_float(orr[k]) * alpha[c + k]);
+                        tmem_st16(tO + c, orr);
+                    }
+                    tmem_wait_st();
+                }
+            }
+#pragma unroll
+            for (int c4 = 0; c4 < N; c4 += 4) {
+                if (c4 < rows) {
+                    const float4 m = *reinterpret_cast<const float4*>(mref + c4);
+                    const float mm[4] = {m.x, m.y, m.z, m.w};
+                    float e[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // a row that has seen no key yet: 2^(-inf - 0) = 0
+                        e[k] = fast_exp2(score(c4 + k) - (mm[k] == -INFINITY ? 0.f : mm[k]));
+                        l[c4 + k] += e[k];
+                    }
+                    const uint32_t a = pack_bf16x2(e[0], e[1]), d = pack_bf16x2(e[2], e[3]);
+                    const uint32_t row = sP + c4 * 128 + in_piece;
+                    st_shared_u16(row + ((piece ^ (c4 & 7)) << 4), (uint16_t)a);
+                    st_shared_u16(row + 128 + ((piece ^ ((c4 + 1) & 7)) << 4), (uint16_t)(a >> 16));
+                    st_shared_u16(row + 256 + ((piece ^ ((c4 + 2) & 7)) << 4), (uint16_t)d);
+                    st_shared_u16(row + 384 + ((piece ^ ((c4 + 3) & 7)) << 4), (uint16_t)(d >> 16));
+                }
+            }
+            fence_async_shared();
+            softmax_arrive<true>(b.p_full(t), lane);
+        }
+        it += un[0] + un[1];
+
+        // ---- sums over the group's keys, then the two groups joined by group 0
+        float m = -INFINITY, sum = 0.f;    // of row r, in the threads r < N
+        if (n > 0) {
+#pragma unroll
+            for (int c4 = 0; c4 < N; c4 += 4) {
+                if (c4 < rows) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float v = l[c4 + k];
+#pragma unroll
+                        for (int off = 16; off > 0; off >>= 1)
+                            v += __shfl_xor_sync(0xffffffffu, v, off);
+                        if (lane == 0) red[quarter * N + c4 + k] = v;
+                    }
+                }
+            }
+            const bool ok = warp_wait(b.o_final(t), o_used[t] & 1, abort_flag);
+            if (group_any(t, !ok)) return;
+            if (r < N && r < rows) {
+                m = mref[r];
+                sum = (red[r] + red[N + r]) + (red[2 * N + r] + red[3 * N + r]);
+            }
+        }
+        const bool both = un[1] > 0;
+        if (t == 1) {
+            if (both) {
+                if (r < N) ml[r] = make_float2(m, sum);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b.ml_full());
+            }
+        } else {
+            if (both) {
+                const bool ok = warp_wait(b.ml_full(), ml_cnt & 1, abort_flag) &&
+                                warp_wait(b.o_final(1), o_used[1] & 1, abort_flag);
+                if (group_any(0, !ok)) return;
+                ++ml_cnt;
+            }
+            if (r < N && r < rows) {
+                float w0 = n > 0 ? 1.f : 0.f, w1 = 0.f;
+                if (both) {
+                    const float2 o = ml[r];
+                    const float mn = fmaxf(m, o.x), mb = mn == -INFINITY ? 0.f : mn;
+                    w0 = fast_exp2(m - mb);
+                    w1 = fast_exp2(o.x - mb);
+                    sum = sum * w0 + o.y * w1;
+                    m = mn;
+                }
+                const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+                weight[r] = make_float2(w0 * inv, w1 * inv);
+                const float lse = sum != 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+                if (slot < 0) {
+                    const int tk = r / p.G;
+                    const size_t row = (size_t)(tok0 + tk) * p.Hq + hk * p.G + (r - tk * p.G);
+                    if (dcheck(row < (size_t)p.T * p.Hq)) p.lse[row] = lse;
+                } else if (dcheck(slot < 2 * kPagedMaxCtas)) {
+                    p.part_lse[(size_t)slot * 256 + r] = lse;
+                }
+            }
+            group_sync(0);
+            tc_fence_after_sync();
+            const int dim = D == 128 ? r : quarter * 16 + lane;
+            const bool has_dim = D == 128 || lane < 16;
+            size_t row = slot < 0 ? (size_t)tok0 * p.Hq + hk * p.G : (size_t)slot * 256;
+            int head = 0;
+#pragma unroll 1
+            for (int c0 = 0; c0 < rows; c0 += 16) {
+                uint32_t o0[16], o1[16];
+                if (n > 0) {
+                    tmem_ld16(tO + c0, o0);
+                    tmem_wait_ld16(o0);
+                }
+                if (both) {
+                    tmem_ld16(tO1 + c0, o1);
+                    tmem_wait_ld16(o1);
+                }
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    if (c0 + c < rows) {
+                        const float2 w = weight[c0 + c];
+                        float v = n > 0 ? __uint_as_float(o0[c]) * w.x : 0.f;
+                        if (both) v = fmaf(__uint_as_float(o1[c]), w.y, v);
+                        if (slot < 0) {
+                            if (has_dim && dcheck(row < (size_t)p.T * p.Hq))
+                                p.o[row * D + dim] = (uint16_t)pack_bf16x2(v, 0.f);
+                            ++row;
+                            if (++head == p.G) {     // the group's heads of the next token
+                                head = 0;
+                                row += p.Hq - p.G;
+                            }
+                        } else {
+                            if (has_dim && dcheck(row < (size_t)512 * kPagedMaxCtas))
+                                p.part_o[row * D + dim] = v;
+                            ++row;
+                        }
+                    }
+                }
+            }
+            group_sync(0);       // the weights are read
+            if (n > 0) softmax_arrive<true>(b.o_free(0), lane);
+            if (both) softmax_arrive<true>(b.o_free(1), lane);
+        }
+        for (int k = 0; k < 2; ++k)
+            if (un[k] > 0) ++o_used[k];
+    }
+}
+
+// ---------------------------------------------------------------- kernel --
+template <int D, int N, bool SPARSE>
+__global__ void __launch_bounds__(kPagedThreads, 1)
+    attn_paged_rows_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
+                                 const __grid_constant__ CUtensorMap tm_k,
+                                 const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+    using T = PagedTraits<D, N>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    PagedBars<T> b;
+    b.base = smem_addr(smem + T::kOffBars);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + T::kOffMisc);
+    PagedShared sh;
+    sh.smem = smem;
+    sh.abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    sh.tail_info = reinterpret_cast<int*>(tmem_holder + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) paged_init<T>(b, sh);
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_addr(tmem_holder), 256);
+        tmem_relinquish();
+    }
+    // Q rows that no copy ever writes are zeros, so their columns stay finite
+    for (int i = threadIdx.x; i < 2 * T::kQBytes / 16; i += kPagedThreads)
+        reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    fence_async_shared();
+    // P's area is free until the first tile
+    const PagedStretch st = paged_schedule(p, reinterpret_cast<long long*>(smem + T::kOffStage));
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tbase = *tmem_holder;
+
+    // 64 columns of scores and of sums: more registers for the softmax warpgroups
+    if constexpr (N == 64) {
+        if (warp < 8) regs_increase<T::kSoftmaxRegs>();
+        else regs_decrease<T::kOtherRegs>();
+    }
+    if (warp < 8)
+        rows_softmax<D, N>(p, tbase, b, sh, warp, lane);
+    else if (warp == 8)
+        paged_producer<T, SPARSE>(p, st, &tm_q, &tm_k, &tm_v, b, sh, lane);
+    else if (warp == 9 || warp == 11) {
+        if (lane == 0) rows_mma<D, N>(tbase, b, sh, warp == 9 ? 0 : 1);
+    } else
+        paged_tail<T>(b, sh, lane);
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == 9) {
+        __syncwarp();
+        tmem_dealloc(tbase, 256);
+    }
+}
+
+}  // namespace eattn
