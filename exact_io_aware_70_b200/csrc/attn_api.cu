@@ -129,7 +129,7 @@ bool encode_q_map(CUtensorMap* map, const void* base, int T, int Hq, int D, long
 
 struct DeviceInfo {
     int sms = 0;
-    bool paged_attr_set[16] = {};
+    bool paged_attr_set[12] = {};
     bool tables_attr_set = false;
     bool score_attr_set[2] = {false, false};
     bool fwd_attr_set[8] = {false, false, false, false, false, false, false, false};
@@ -705,7 +705,7 @@ attn_status_t launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const C
         if (di.sms == 0 &&
             cudaDeviceGetAttribute(&di.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return ATTN_ERR_CUDA;
-        const int slot = (N == 16 ? 4 : N == 32 ? 8 : N == 64 ? 12 : 0) + (SPARSE ? 2 : 0) +
+        const int slot = (N == 16 ? 4 : N == 32 ? 8 : 0) + (SPARSE ? 2 : 0) +
                          (D == 128 ? 1 : 0);
         if (!di.paged_attr_set[slot]) {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -729,7 +729,6 @@ attn_status_t launch_paged_rows(int rows, const CUtensorMap& tq, const CUtensorM
     switch (rows) {
         case 16: return launch_paged<D, 16, SPARSE>(tq, tk, tv, p, st);
         case 32: return launch_paged<D, 32, SPARSE>(tq, tk, tv, p, st);
-        case 64: return launch_paged<D, 64, SPARSE>(tq, tk, tv, p, st);
     }
     return launch_paged<D, 0, SPARSE>(tq, tk, tv, p, st);
 }
@@ -768,7 +767,7 @@ attn_status_t paged_entry(const void* q, const void* k_cache, const void* v_cach
     // Rows of a unit: with few tokens per sequence (on average; the lengths are on the
     // device) the turned kernel, whose work follows the rows in use, else 128-row tiles.
     const long long avg = sel ? 1 : (T + (long long)B - 1) / B;
-    const int rows = avg * G <= 16 ? 16 : avg * G <= 32 ? 32 : avg * G <= 64 ? 64 : 0;
+    const int rows = avg * G <= 16 ? 16 : G <= 32 && avg * G <= 64 ? 32 : 0;
     p.tpt = sel ? 1 : (rows ? rows : 128) / G;
     p.unit_tok = sel || rows ? p.tpt : 2 * p.tpt;
     const int box = page_size < 128 ? page_size : 128;

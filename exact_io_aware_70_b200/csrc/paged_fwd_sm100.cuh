@@ -75,7 +75,7 @@ struct PagedParams {
     float scale_log2;
 };
 
-// N = 0: 128-row Q tiles (this file); N = 16, 32, 64: at most N rows per unit, kept as columns
+// N = 0: 128-row Q tiles (this file); N = 16, 32: at most N rows per unit, kept as columns
 // (paged_rows_sm100.cuh).
 template <int D, int N = 0>
 struct PagedTraits {
@@ -213,6 +213,7 @@ struct PagedLine {
 struct PagedStretch {
     long long offset, length;
     int b;
+    int block;   // sparse: tokens of a block of units (see paged_producer)
 };
 
 // Run by the whole CTA. `red`: kPagedThreads / 32 + 4 words of 64 bits.
@@ -242,6 +243,12 @@ __device__ __forceinline__ PagedStretch paged_schedule(const PagedParams& p, lon
     long long chunk = (total + gridDim.x - 1) / gridDim.x;
     if (chunk < kPagedMinStretch) chunk = kPagedMinStretch;
     PagedStretch st;
+    st.block = 1;
+    if (p.sel) {   // about as many tokens as one stretch holds for all K/V heads
+        const long long all_heads =
+            (kPagedUnitCost + ((long long)p.K << p.page_shift)) * p.Hkv;
+        st.block = (int)min(max((chunk + all_heads / 2) / all_heads, 1ll), 1ll << 20);
+    }
     const long long start = chunk * blockIdx.x;
     st.length = min(chunk, total - start);
     st.offset = 0;
@@ -345,16 +352,35 @@ __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, con
         return true;
     };
 
+    // sparse: the next unit's first 32 list entries and their pages, read while this unit's
+    // tiles stream in
+    bool ahead = false;
+    int ahead_e = -1, ahead_page = -1;
     long long left = st.length;
     if (left > 0) {
         int sb = st.b;
         PagedSeq s = paged_seq(p, sb);
         PagedLine line(p, s);
-        const long long head = line.begin(line.m);
-        int hk = (int)(st.offset / head);
-        long long rem = st.offset - hk * head;
-        int q;
-        {   // the last unit that begins at or before rem
+        // Units of a sequence in order: K/V head by head, and its rows in turn. Sparse
+        // rows go in blocks of st.block tokens, head by head within a block: as a
+        // stretch is about one block long, the CTAs sweep the heads together and
+        // the pages of one head at a time are what L2 has to hold (measured on
+        // 1050 rows of 16 pages of 64, 2 x 15K keys: 718 -> SPARSE_US us).
+        int hk, q, q0 = 0;
+        long long rem = st.offset;
+        if constexpr (SPARSE) {
+            const long long per = (long long)st.block * p.Hkv;
+            const long long i = rem / line.base;
+            rem -= i * line.base;
+            q0 = (int)(i / per) * st.block;
+            const int in = (int)(i - (long long)q0 * p.Hkv), nq = min(st.block, line.m - q0);
+            hk = in / nq;
+            q = q0 + in - hk * nq;
+        } else {
+            const long long head = line.begin(line.m);
+            hk = (int)(rem / head);
+            rem -= hk * head;
+            // the last unit that begins at or before rem
             int lo = 0, hi = line.m - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
@@ -383,15 +409,20 @@ __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, con
                 const int* row = p.sel + ((size_t)u.tok * p.Hkv + hk) * p.K;
                 const int vis = u.pos0 + 1;   // tokens [0, vis) are visible
                 __syncwarp();
+                int next_e = ahead ? ahead_e : lane < p.K ? __ldg(row + lane) : -1;
                 for (int k0 = 0; k0 < p.K; k0 += 32) {
-                    const int e = k0 + lane < p.K ? __ldg(row + k0 + lane) : -1;
+                    const int e = next_e;
+                    if (k0 + 32 + lane < p.K) next_e = __ldg(row + k0 + 32 + lane);
+                    else next_e = -1;
                     const long long t0 = (long long)e << p.page_shift;   // first token of the page
                     bool ok = e >= 0 && t0 < u.len;
                     if (!ok && e != -1) atomicOr(&g_attn_status, kDevErrBadIndex);
                     ok = ok && t0 < vis;
                     int page = -1, nv = 0;
                     if (ok) {
-                        page = __ldg(p.block_table + (size_t)sb * p.max_pages + e);
+                        page = ahead && k0 == 0
+                                   ? ahead_page
+                                   : __ldg(p.block_table + (size_t)sb * p.max_pages + e);
                         if (page < 0 || page >= p.num_pages)
                             atomicOr(&g_attn_status, kDevErrBadIndex);
                         else
@@ -453,6 +484,27 @@ __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, con
                 }
             }
             if (!publish(u)) goto fail;
+            int ahead_pos = -1;
+            if constexpr (SPARSE) {
+                // the next unit's token and head, if it is in this sequence
+                const bool wrap = q + 1 == min(q0 + st.block, line.m);
+                const bool next_block = wrap && hk + 1 == p.Hkv;
+                ahead = left > p1 - p0 && !(next_block && q + 1 == line.m);
+                if (ahead) {
+                    const int nq = !wrap || next_block ? q + 1 : q0;
+                    const int nh = next_block ? 0 : hk + wrap;
+                    ahead_pos = s.len - s.n + nq;
+                    ahead_e = lane < p.K ? __ldg(p.sel + ((size_t)(s.tok + nq) * p.Hkv + nh) * p.K + lane)
+                                         : -1;
+                }
+            }
+            // the page of entry ahead_e, if the next unit's row can see it
+            auto look_ahead = [&]() {
+                if (SPARSE && ahead && ahead_e >= 0 &&
+                    ((long long)ahead_e << p.page_shift) <= ahead_pos)
+                    ahead_page = __ldg(p.block_table + (size_t)sb * p.max_pages + ahead_e);
+            };
+            if (N == 0) look_ahead();
             if (N > 0) {
                 // Q: token-major rows of the group's heads
                 const int ntile = u.kind == 2 ? 2 : 1;
@@ -559,6 +611,7 @@ __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, con
                         tma_load_3d_hint(sKV + sv * T::kTileBytes + box_off, tv, vbar, panel * 64,
                                          y, z, pol);
                     ++it;
+                    if (j == 0) look_ahead();
                     page = npage;
                     y = ny;
                     keys = nkeys;
@@ -567,16 +620,22 @@ __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, con
             left -= p1 - p0;
             rem = 0;
             if (left <= 0) break;
-            if (++q == line.m) {
-                q = 0;
-                if (++hk == p.Hkv) {
+            // the next unit
+            if (++q == (SPARSE ? min(q0 + st.block, line.m) : line.m)) {
+                if (++hk < p.Hkv) {
+                    q = q0;
+                } else {
                     hk = 0;
-                    do {
-                        if (++sb >= p.B) break;
-                        s = paged_seq(p, sb);
-                    } while (s.n == 0);
-                    if (sb >= p.B) break;
-                    line = PagedLine(p, s);
+                    q0 = q;
+                    if (q == line.m) {
+                        do {
+                            if (++sb >= p.B) break;
+                            s = paged_seq(p, sb);
+                        } while (s.n == 0);
+                        if (sb >= p.B) break;
+                        line = PagedLine(p, s);
+                        q = q0 = 0;
+                    }
                 }
             }
         }

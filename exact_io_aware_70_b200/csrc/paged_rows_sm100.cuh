@@ -1,7 +1,7 @@
 // paged_rows_sm100.cuh -- attention of few rows over a paged K/V cache: decode,
 // drafted tokens, and rows that each read pages of their own.
 //
-// The same sums as paged_fwd_sm100.cuh, for units of at most N = 16, 32 or 64
+// The same sums as paged_fwd_sm100.cuh, for units of at most N = 16 or 32
 // rows (token, head of the group). There, 128 rows of a tile are computed
 // whatever the unit has, and the thread of a row takes its 128 scores one after
 // another: with 4 rows of 128 in use that thread sets the pace (1.4 us per key
@@ -20,6 +20,8 @@
 // The two softmax groups take alternate key tiles, each with its own issuing
 // thread, so neither waits for the other; group 0 joins the results.
 #pragma once
+
+#include <cfloat>
 
 #include "paged_fwd_sm100.cuh"
 
@@ -46,18 +48,36 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
+// The largest of a warp's 32 values, in every lane (NaN ignored).
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Sums of 16 values over a warp: lane l ends with the sum of value l / 2.
+__device__ __forceinline__ float warp_sum16(float (&v)[16], int lane) {
+#pragma unroll
+    for (int half = 8; half >= 1; half >>= 1) {
+        const bool hi = (lane & (2 * half)) != 0;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float send = hi ? v[i] : v[i + half], keep = hi ? v[i + half] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * half);
+        }
+    }
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
 // N consecutive columns of this warp's 32 tensor-memory lanes
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
     if constexpr (N == 16) {
         tmem_ld16(taddr, r);
         tmem_wait_ld16(r);
-    } else if constexpr (N == 32) {
+    } else {
         tmem_ld32(taddr, r);
         tmem_wait_ld(r);
-    } else {
-        tmem_ld64(taddr, r);
-        tmem_wait_ld64(r);
     }
 }
 // ------------------------------------------------------------ MMA issuer --
@@ -169,15 +189,18 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
     const volatile uint32_t* masks =
         reinterpret_cast<const volatile uint32_t*>(sh.smem + T::kOffMask);
     // per row: group 1's (m, l) and group 0's weights (apart: group 1 may be a unit ahead);
-    // per group: the reference maximum, the factor of a rescaling, a word per warp for reductions
+    // per group: the negated reference maximum (the lowest float before the
+    // first key: every score is far above it), the factor of a rescaling, a word per warp
     float2* ml = reinterpret_cast<float2*>(sh.smem + T::kOffMl);
     float2* weight = ml + N;
-    float* mref = reinterpret_cast<float*>(sh.smem + T::kOffMl + 2 * N * 8) + t * 6 * N;
-    float* alpha = mref + N;
+    float* minus_ref = reinterpret_cast<float*>(sh.smem + T::kOffMl + 2 * N * 8) + t * 6 * N;
+    float* alpha = minus_ref + N;
     float* red = alpha + N;
     // where key r of row c goes in P: 128-byte rows of 64 keys, 16-byte pieces swizzled by row
-    const uint32_t sP = smem_addr(sh.smem) + T::kOffStage + t * N * 256 + (r >> 6) * N * 128;
-    const uint32_t piece = (r & 63) >> 3, in_piece = (r & 7) * 2;
+    const uint32_t sP =
+        smem_addr(sh.smem) + T::kOffStage + t * N * 256 + (r >> 6) * N * 128 + (r & 7) * 2;
+    const uint32_t piece = (r & 63) >> 3;
+    constexpr int kChunk = N == 16 ? 8 : 16;    // columns skipped together when no row has them
     const float c2 = p.scale_log2;
     uint32_t it = 0, s_cnt = 0, ml_cnt = 0;
     uint32_t o_used[2] = {0, 0};
@@ -185,7 +208,7 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
     for (uint32_t units = 0;; ++units) {
         const int ri = units % T::kUnits;
         const bool got = warp_wait(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag);
-        if (r < N) mref[r] = -INFINITY;
+        if (r < N) minus_ref[r] = FLT_MAX;
         if (group_any(t, !got)) return;
         const volatile PagedUnit& uu = ring[ri];
         const int kind = uu.kind, hk = uu.hk, tok0 = uu.tok, ntok = uu.ntok, pos0 = uu.pos0;
@@ -209,54 +232,76 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
             ok = ok && warp_wait(b.s_full(t), s_cnt & 1, abort_flag);
             ++s_cnt;
             tc_fence_after_sync();
-            uint32_t sr[N];
-            tmem_ld_cols<N>(tS, sr);
-            // the score of column c in log2 units
-            auto score = [&](int c) { return c >= first ? __uint_as_float(sr[c]) * c2 : -INFINITY; };
-            bool over = !ok;
+            // exponents of every column in use, and whether one of them is above 2^8
+            const bool masked = __any_sync(0xffffffffu, first > 0);
+            float arg[N];
+            auto exponents = [&]() -> bool {
+                float top = -INFINITY;
+                uint32_t sr[N];
+                tmem_ld_cols<N>(tS, sr);
 #pragma unroll
-            for (int c4 = 0; c4 < N; c4 += 4) {
-                if (c4 < rows) {
-                    const float4 m = *reinterpret_cast<const float4*>(mref + c4);
-                    const float mm[4] = {m.x, m.y, m.z, m.w};
+                for (int c0 = 0; c0 < N; c0 += kChunk) {
+                    if (c0 < rows) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) over |= score(c4 + k) > mm[k] + 8.0f;
-                }
-            }
-            if (group_any(t, over)) {
-                if (group_any(t, !ok)) return;
-                // the reference of every row moves to its maximum so far
-#pragma unroll
-                for (int c4 = 0; c4 < N; c4 += 4) {
-                    if (c4 < rows) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float v = score(c4 + k);
-#pragma unroll
-                            for (int off = 16; off > 0; off >>= 1)
-                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-                            if (lane == 0) red[quarter * N + c4 + k] = v;
+                        for (int c = c0; c < c0 + kChunk; c += 4) {
+                            const float4 m = *reinterpret_cast<const float4*>(minus_ref + c);
+                            arg[c] = fmaf(__uint_as_float(sr[c]), c2, m.x);
+                            arg[c + 1] = fmaf(__uint_as_float(sr[c + 1]), c2, m.y);
+                            arg[c + 2] = fmaf(__uint_as_float(sr[c + 2]), c2, m.z);
+                            arg[c + 3] = fmaf(__uint_as_float(sr[c + 3]), c2, m.w);
                         }
+                        if (masked) {
+#pragma unroll
+                            for (int c = c0; c < c0 + kChunk; ++c)
+                                if (c < first) arg[c] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int c = c0; c < c0 + kChunk; c += 2)
+                            top = fmax3(top, arg[c], arg[c + 1]);
                     }
                 }
+                return top > 8.0f;
+            };
+            for (bool again = false;; again = true) {
+                const bool over = exponents();
+                if (again || !group_any(t, over || !ok)) break;
+                if (group_any(t, !ok)) return;
+                // the reference of every row moves to its maximum so far
+#pragma unroll 1
+                for (int c0 = 0; c0 < rows; c0 += 16) {
+                    uint32_t sr[16];
+                    tmem_ld16(tS + c0, sr);
+                    tmem_wait_ld16(sr);
+                    float mine = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float v = warp_max(
+                            c0 + c >= first ? __uint_as_float(sr[c]) * c2 : -INFINITY);
+                        if (lane == c) mine = v;
+                    }
+                    if (lane < 16) red[quarter * N + c0 + lane] = mine;
+                }
                 group_sync(t);
-                if (r < N && r < rows) {
-                    const float m_old = mref[r];
+                if (r < N) {    // columns without a row too: they share their chunk's vote
+                    const float m_old = -minus_ref[r];
                     const float v = fmaxf(fmaxf(red[r], red[N + r]),
                                           fmaxf(red[2 * N + r], red[3 * N + r]));
                     const float m_new = fmaxf(m_old, v);
-                    alpha[r] = m_new == -INFINITY ? 1.0f : fast_exp2(m_old - m_new);
-                    mref[r] = m_new;
+                    alpha[r] = fast_exp2(m_old - m_new);
+                    minus_ref[r] = -m_new;
                 }
                 group_sync(t);
 #pragma unroll
-                for (int c4 = 0; c4 < N; c4 += 4) {
-                    if (c4 < rows) {
-                        const float4 a = *reinterpret_cast<const float4*>(alpha + c4);
-                        l[c4] *= a.x;
-                        l[c4 + 1] *= a.y;
-                        l[c4 + 2] *= a.z;
-                        l[c4 + 3] *= a.w;
+                for (int c0 = 0; c0 < N; c0 += kChunk) {
+                    if (c0 < rows) {
+#pragma unroll
+                        for (int c = c0; c < c0 + kChunk; c += 4) {
+                            const float4 a = *reinterpret_cast<const float4*>(alpha + c);
+                            l[c] *= a.x;
+                            l[c + 1] *= a.y;
+                            l[c + 2] *= a.z;
+                            l[c + 3] *= a.w;
+                        }
                     }
                 }
                 if (i > 0) {      // S(i) is complete, so P(i-1) V is
@@ -274,23 +319,18 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
                 }
             }
 #pragma unroll
-            for (int c4 = 0; c4 < N; c4 += 4) {
-                if (c4 < rows) {
-                    const float4 m = *reinterpret_cast<const float4*>(mref + c4);
-                    const float mm[4] = {m.x, m.y, m.z, m.w};
-                    float e[4];
+            for (int c0 = 0; c0 < N; c0 += kChunk) {
+                if (c0 < rows) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // a row that has seen no key yet: 2^(-inf - 0) = 0
-                        e[k] = fast_exp2(score(c4 + k) - (mm[k] == -INFINITY ? 0.f : mm[k]));
-                        l[c4 + k] += e[k];
+                    for (int c = c0; c < c0 + kChunk; c += 2) {
+                        const float e0 = fast_exp2(arg[c]), e1 = fast_exp2(arg[c + 1]);
+                        l[c] += e0;
+                        l[c + 1] += e1;
+                        const uint32_t pk = pack_bf16x2(e0, e1);
+                        st_shared_u16(sP + c * 128 + ((piece ^ (c & 7)) << 4), (uint16_t)pk);
+                        st_shared_u16(sP + (c + 1) * 128 + ((piece ^ ((c + 1) & 7)) << 4),
+                                      (uint16_t)(pk >> 16));
                     }
-                    const uint32_t a = pack_bf16x2(e[0], e[1]), d = pack_bf16x2(e[2], e[3]);
-                    const uint32_t row = sP + c4 * 128 + in_piece;
-                    st_shared_u16(row + ((piece ^ (c4 & 7)) << 4), (uint16_t)a);
-                    st_shared_u16(row + 128 + ((piece ^ ((c4 + 1) & 7)) << 4), (uint16_t)(a >> 16));
-                    st_shared_u16(row + 256 + ((piece ^ ((c4 + 2) & 7)) << 4), (uint16_t)d);
-                    st_shared_u16(row + 384 + ((piece ^ ((c4 + 3) & 7)) << 4), (uint16_t)(d >> 16));
                 }
             }
             fence_async_shared();
@@ -302,22 +342,19 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
         float m = -INFINITY, sum = 0.f;    // of row r, in the threads r < N
         if (n > 0) {
 #pragma unroll
-            for (int c4 = 0; c4 < N; c4 += 4) {
-                if (c4 < rows) {
+            for (int c0 = 0; c0 < N; c0 += 16) {
+                if (c0 < rows) {
+                    float v[16];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float v = l[c4 + k];
-#pragma unroll
-                        for (int off = 16; off > 0; off >>= 1)
-                            v += __shfl_xor_sync(0xffffffffu, v, off);
-                        if (lane == 0) red[quarter * N + c4 + k] = v;
-                    }
+                    for (int c = 0; c < 16; ++c) v[c] = l[c0 + c];
+                    const float x = warp_sum16(v, lane);
+                    if ((lane & 1) == 0) red[quarter * N + c0 + (lane >> 1)] = x;
                 }
             }
             const bool ok = warp_wait(b.o_final(t), o_used[t] & 1, abort_flag);
             if (group_any(t, !ok)) return;
             if (r < N && r < rows) {
-                m = mref[r];
+                m = -minus_ref[r];
                 sum = (red[r] + red[N + r]) + (red[2 * N + r] + red[3 * N + r]);
             }
         }
@@ -444,11 +481,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     tc_fence_after_sync();
     const uint32_t tbase = *tmem_holder;
 
-    // 64 columns of scores and of sums: more registers for the softmax warpgroups
-    if constexpr (N == 64) {
-        if (warp < 8) regs_increase<T::kSoftmaxRegs>();
-        else regs_decrease<T::kOtherRegs>();
-    }
     if (warp < 8)
         rows_softmax<D, N>(p, tbase, b, sh, warp, lane);
     else if (warp == 8)
