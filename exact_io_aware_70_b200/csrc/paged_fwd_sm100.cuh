@@ -42,12 +42,11 @@
 
 namespace eattn {
 
-constexpr int kPagedThreads = 384;
 constexpr int kPagedMaxCtas = 160;     // slots of the workspace; the grid is at most this
 // Cost of starting a unit, and the least stretch worth a CTA of its own, in keys.
 constexpr int kPagedUnitCost = 128;
 constexpr int kPagedMinStretch = 512;
-constexpr int kPagedListMax = 1024;    // entries of a sparse row's list of key runs
+constexpr int kPagedListMax = 480;     // entries of a sparse row's list of key runs
 
 // One CTA's partial rows of a unit that its stretch covers only in part.
 // Slot 2c: a piece that continues a unit begun by an earlier CTA; slot 2c + 1: one that
@@ -87,7 +86,11 @@ struct PagedTraits {
     static constexpr int kPairs = D == 128 ? (N == 16 ? 3 : 2) : N == 16 ? 6 : N == 32 ? 5 : 4;
     static constexpr int kSlots = 2 * kPairs;
     static constexpr int kUnits = 4;                     // unit records in flight
-    static constexpr int kMasks = 2 * kPairs;
+    // the mask ring is longer than the K/V ring by the tiles that units planned ahead can have
+    // without any work for one of the groups (kUnits, one tile each)
+    static constexpr int kMasks = 2 * kPairs + 2 * kUnits;
+    static constexpr int kThreads = N ? 416 : 384;       // a 13th warp plans; else warp 11 does
+    static constexpr int kPlanner = N ? 12 : 11;
     static constexpr int kQRows = N ? N : 128;
     static constexpr int kQPanelBytes = kQRows * 128;
     static constexpr int kQBytes = kPanels * kQPanelBytes;    // one Q slot (of two)
@@ -95,12 +98,12 @@ struct PagedTraits {
     static constexpr int kStageWarpBytes = 32 * 64;
     // N = 0: the epilogue's staging blocks; else P of both softmax groups (N x 128 bf16 each)
     static constexpr int kStageBytes = N ? 2 * N * 256 : 8 * kStageWarpBytes;
-    static constexpr int kMlBytes = N ? 2 * N * 8 + 2 * 6 * N * 4 : 128 * 8;
-    static constexpr int kBars = 2 * kSlots + kPairs + 4 + 4 + 8 + 2 * kUnits + 2 + 2 * kMasks;
+    static constexpr int kMlBytes = N ? 3 * N * 8 + 2 * 6 * N * 4 : 128 * 8;
+    static constexpr int kBars = 2 * kSlots + kPairs + 4 + 4 + 8 + 2 * kUnits + 3 + 2 * kMasks;
     static constexpr int kOffKV = 2 * kQBytes;
     static constexpr int kOffStage = kOffKV + kSlots * kTileBytes;
     static constexpr int kOffList = kOffStage + kStageBytes;
-    static constexpr int kOffMl = kOffList + kPagedListMax * 8;
+    static constexpr int kOffMl = kOffList + kUnits * kPagedListMax * 8;
     static constexpr int kOffMask = kOffMl + kMlBytes;
     static constexpr int kOffUnits = kOffMask + kMasks * 16;
     static constexpr int kOffBars = kOffUnits + kUnits * 64;
@@ -110,7 +113,7 @@ struct PagedTraits {
     // as in the dense forward: the launch gives every thread 168 registers (the
     // build checks it) and the warpgroups redistribute them
     static constexpr int kLaunchRegs = 168, kSoftmaxRegs = 192, kOtherRegs = 120;
-    static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kPagedThreads * kLaunchRegs,
+    static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= 384 * kLaunchRegs,
                   "register split exceeds the launch allocation");
     static constexpr uint32_t kColS0 = 0, kColS1 = N ? 64 : 128, kColO0 = N ? 128 : 256,
                               kColO1 = N ? 192 : 384;
@@ -136,21 +139,22 @@ struct PagedBars {
     __device__ __forceinline__ uint32_t unit_empty(int i) const {
         return at(kA + 16 + T::kUnits + i);
     }
-    __device__ __forceinline__ uint32_t ml_full() const { return at(kA + 16 + 2 * T::kUnits); }
-    __device__ __forceinline__ uint32_t drain() const { return at(kA + 17 + 2 * T::kUnits); }
+    // the joining group's (m, l) of the other one's rows are there
+    __device__ __forceinline__ uint32_t ml_full(int t) const { return at(kA + 16 + 2 * T::kUnits + t); }
+    __device__ __forceinline__ uint32_t drain() const { return at(kA + 18 + 2 * T::kUnits); }
     // Key tile x of the CTA: its mask is written and its K slot has been given to it
     // (entry x % kMasks), and the same for its V slot. A parity tells only the
     // last two uses of a slot apart, so a thread that has not itself waited for the
     // slot's previous use waits for these first.
     __device__ __forceinline__ uint32_t mask_full(int i) const {
-        return at(kA + 18 + 2 * T::kUnits + i);
+        return at(kA + 19 + 2 * T::kUnits + i);
     }
     __device__ __forceinline__ uint32_t v_given(int i) const {
-        return at(kA + 18 + 2 * T::kUnits + T::kMasks + i);
+        return at(kA + 19 + 2 * T::kUnits + T::kMasks + i);
     }
 };
 
-// A unit (or the piece of one) that the CTA works on, handed from the producer
+// A unit (or the piece of one) that the CTA works on, handed from the planner
 // to the other roles through a ring in shared memory.
 struct PagedUnit {
     int kind;        // 0: end of the CTA's work; 1: narrow; 2: wide
@@ -162,7 +166,9 @@ struct PagedUnit {
     int n0, n1;      // key tiles of Q tile / softmax group 0 and 1
     int slot;        // -1: whole unit; else the workspace slot of its partial rows
     int qs;          // Q slot of a narrow unit
-    int pad[5];
+    int seq, keys;   // sequence and its keys
+    int entries;     // sparse: runs in the unit's list
+    int pad[2];
 };
 static_assert(sizeof(PagedUnit) == 64, "unit record");
 
@@ -216,9 +222,10 @@ struct PagedStretch {
     int block;   // sparse: tokens of a block of units (see paged_producer)
 };
 
-// Run by the whole CTA. `red`: kPagedThreads / 32 + 4 words of 64 bits.
+// Run by the whole CTA. `red`: THREADS / 32 + 2 words of 64 bits.
+template <int THREADS>
 __device__ __forceinline__ PagedStretch paged_schedule(const PagedParams& p, long long* red) {
-    constexpr int kWarps = kPagedThreads / 32;
+    constexpr int kWarps = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto cost = [&](int b, bool report) -> long long {
         const PagedSeq s = paged_seq(p, b);
@@ -227,7 +234,7 @@ __device__ __forceinline__ PagedStretch paged_schedule(const PagedParams& p, lon
         return p.Hkv * line.begin(line.m);
     };
     long long mine = 0, first = 0;
-    for (int b = tid; b < p.B; b += kPagedThreads) {
+    for (int b = tid; b < p.B; b += THREADS) {
         const long long c = cost(b, blockIdx.x == 0);
         if (b == tid) first = c;
         mine += c;
@@ -258,7 +265,7 @@ __device__ __forceinline__ PagedStretch paged_schedule(const PagedParams& p, lon
         return st;
     }
     long long before = 0;
-    for (int b0 = 0; b0 < p.B && before <= start; b0 += kPagedThreads) {
+    for (int b0 = 0; b0 < p.B && before <= start; b0 += THREADS) {
         const int b = b0 + tid;
         const long long v = b < p.B ? (b0 == 0 ? first : cost(b, false)) : 0;
         long long incl = v;
@@ -309,14 +316,212 @@ __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-// The producer warp, all lanes together.
+// The units of a CTA's stretch in order. Dense: K/V head by head, and a head's
+// rows in turn. Sparse: blocks of `block` tokens, head by head within a block:
+// as a stretch is about one block long, the CTAs sweep the heads together and L2
+// holds the pages of one head at a time.
+template <bool SPARSE>
+struct PagedWalk {
+    PagedSeq s;
+    PagedLine line;
+    int sb, hk, q, q0, block;
+    long long rem, left;     // where in unit q the stretch stands, and what is left of it
+
+    __device__ __forceinline__ PagedWalk(const PagedParams& p, const PagedStretch& st)
+        : s(paged_seq(p, st.b)), line(p, s), sb(st.b), hk(0), q(0), q0(0), block(st.block),
+          rem(st.offset), left(st.length) {
+        if (left <= 0) return;
+        if constexpr (SPARSE) {
+            const long long i = rem / line.base;      // units before this one
+            rem -= i * line.base;
+            q0 = (int)(i / ((long long)block * p.Hkv)) * block;
+            const int in = (int)(i - (long long)q0 * p.Hkv), nq = min(block, line.m - q0);
+            hk = in / nq;
+            q = q0 + in - hk * nq;
+        } else {
+            const long long head = line.begin(line.m);
+            hk = (int)(rem / head);
+            rem -= hk * head;
+            // the last unit that begins at or before rem
+            int hi = line.m - 1;
+            while (q < hi) {
+                const int mid = (q + hi + 1) >> 1;
+                if (line.begin(mid) <= rem) q = mid;
+                else hi = mid - 1;
+            }
+            rem -= line.begin(q);
+        }
+    }
+    // past the part of unit q that [rem, rem + taken) is
+    __device__ __forceinline__ void advance(const PagedParams& p, long long taken) {
+        left -= taken;
+        rem = 0;
+        if (left <= 0) return;
+        if (++q < (SPARSE ? min(q0 + block, line.m) : line.m)) return;
+        if (++hk < p.Hkv) {
+            q = q0;
+            return;
+        }
+        hk = 0;
+        q0 = q;
+        if (q < line.m) return;
+        q = q0 = 0;
+        do {
+            if (++sb >= p.B) {
+                left = 0;
+                return;
+            }
+            s = paged_seq(p, sb);
+        } while (s.n == 0);
+        line = PagedLine(p, s);
+    }
+};
+
+// The planner warp, all lanes together: the units one after another, up to kUnits
+// ahead (planning a unit takes a few microseconds of dependent steps), and for sparse
+// rows the lists of their pages.
 template <class T, bool SPARSE>
-__device__ void paged_producer(const PagedParams& p, const PagedStretch& st, const CUtensorMap* tq,
-                               const CUtensorMap* tk, const CUtensorMap* tv,
-                               const PagedBars<T>& b, const PagedShared& sh, int lane) {
-    const uint32_t sQ = smem_addr(sh.smem), sKV = sQ + T::kOffKV;
+__device__ void paged_planner(const PagedParams& p, const PagedStretch& st, const PagedBars<T>& b,
+                              const PagedShared& sh, int lane) {
     PagedUnit* ring = reinterpret_cast<PagedUnit*>(sh.smem + T::kOffUnits);
-    int2* list = reinterpret_cast<int2*>(sh.smem + T::kOffList);
+    const int ps = 1 << p.page_shift;
+    const int rshift = min(p.page_shift, 7);      // rows of a box: min(page_size, 128)
+    const int R = 1 << rshift;
+    int qs = 0;
+
+    if (lane < 2) p.pieces[2 * blockIdx.x + lane].valid = 0;
+    __syncwarp();
+
+    PagedWalk<SPARSE> w(p, st);
+    for (uint32_t units = 0;; ++units) {
+        const int ri = units % T::kUnits;
+        PagedUnit u;
+        u.kind = 0;
+        const bool more = w.left > 0;
+        // sparse: the row's first 32 entries and their pages, read while the ring is full
+        int ahead_e = -1, ahead_page = -1;
+        auto visible = [&](int e) {   // (and so in the table)
+            return e >= 0 && ((long long)e << p.page_shift) <= w.s.len - w.s.n + w.q;
+        };
+        auto page_of = [&](int e) { return __ldg(p.block_table + (size_t)w.sb * p.max_pages + e); };
+        if (SPARSE && more && lane < p.K) {
+            ahead_e = __ldg(p.sel + ((size_t)(w.s.tok + w.q) * p.Hkv + w.hk) * p.K + lane);
+            if (visible(ahead_e)) ahead_page = page_of(ahead_e);
+        }
+        if (units >= (uint32_t)T::kUnits &&
+            !warp_wait(b.unit_empty(ri), (units / T::kUnits - 1) & 1, sh.abort_flag))
+            return;
+        if (more) {
+            const long long ulen = w.line.unit(w.q);
+            const long long p0 = w.rem, p1 = min(ulen, w.rem + w.left);
+            u.seq = w.sb;
+            u.keys = u.len = w.s.len;
+            u.hk = w.hk;
+            u.tok = w.s.tok + w.q * w.line.U;
+            u.ntok = min(w.line.U, w.s.n - w.q * w.line.U);
+            u.pos0 = w.s.len - w.s.n + w.q * w.line.U;
+            u.kind = u.ntok > p.tpt ? 2 : 1;
+            u.qs = 0;
+            u.entries = 0;
+            int tiles[2];        // key tiles of the whole unit, for each Q tile
+            if constexpr (SPARSE) {
+                // the row's visible pages as runs of up to R keys: (page, first row, keys)
+                int2* list = reinterpret_cast<int2*>(sh.smem + T::kOffList) + ri * kPagedListMax;
+                const int* row = p.sel + ((size_t)u.tok * p.Hkv + u.hk) * p.K;
+                int next_e = ahead_e;
+                for (int k0 = 0; k0 < p.K; k0 += 32) {
+                    const int e = next_e;
+                    next_e = k0 + 32 + lane < p.K ? __ldg(row + k0 + 32 + lane) : -1;
+                    if (e != -1 && (e < 0 || ((long long)e << p.page_shift) >= u.len))
+                        atomicOr(&g_attn_status, kDevErrBadIndex);
+                    int page = -1, nv = 0;
+                    if (visible(e)) {
+                        page = k0 == 0 ? ahead_page : page_of(e);
+                        if (page < 0 || page >= p.num_pages)
+                            atomicOr(&g_attn_status, kDevErrBadIndex);
+                        else
+                            nv = min(ps, u.pos0 + 1 - (e << p.page_shift));
+                    }
+                    const int runs = (nv + R - 1) >> rshift;
+                    int at = u.entries;
+                    if (rshift == p.page_shift) {     // a page is one run
+                        const unsigned full = __ballot_sync(0xffffffffu, runs > 0);
+                        at += __popc(full & ((1u << lane) - 1));
+                        u.entries += __popc(full);
+                    } else {
+                        int incl = runs;
+#pragma unroll
+                        for (int off = 1; off < 32; off <<= 1) {
+                            const int v = __shfl_up_sync(0xffffffffu, incl, off);
+                            if (lane >= off) incl += v;
+                        }
+                        at += incl - runs;
+                        u.entries += __shfl_sync(0xffffffffu, incl, 31);
+                    }
+                    for (int r = 0; r < runs; ++r)
+                        if (dcheck(at + r < kPagedListMax))
+                            list[at + r] =
+                                make_int2(page, (r << rshift << 8) | min(R, nv - (r << rshift)));
+                }
+                __syncwarp();
+                tiles[0] = (u.entries * R + 127) >> 7;
+                tiles[1] = 0;
+                u.len = 0x7fffffff;   // the masks say it all
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    int vis = 0;
+                    if (u.ntok > t * p.tpt)
+                        vis = p.causal ? u.pos0 + min((t + 1) * p.tpt, u.ntok) : u.len;
+                    tiles[t] = (max(vis, 0) + 127) >> 7;
+                }
+            }
+            const int all = max(tiles[0], tiles[1]);
+            auto tile_at = [&](long long pos) -> int {
+                const long long k = (pos - kPagedUnitCost) >> 7;
+                return k < 0 ? 0 : k > all ? all : (int)k;
+            };
+            const int k0 = p0 == 0 ? 0 : tile_at(p0);
+            const int N = (p1 == ulen ? all : tile_at(p1)) - k0;
+            u.key0 = k0 << 7;
+            if (u.kind == 2) {
+                u.n0 = min(max(tiles[0] - k0, 0), N);
+                u.n1 = min(max(tiles[1] - k0, 0), N);
+            } else {
+                u.n0 = (N + 1) >> 1;
+                u.n1 = N >> 1;
+                u.qs = qs;
+                if (N > 0) qs ^= 1;
+            }
+            u.slot = -1;
+            if (p0 > 0 || p1 < ulen) {
+                u.slot = 2 * blockIdx.x + (p0 > 0 ? 0 : 1);
+                if (lane == 0 && dcheck(u.slot < 2 * kPagedMaxCtas)) {
+                    PagedPiece* pc = p.pieces + u.slot;
+                    pc->last = p1 == ulen ? 1 : 0;
+                    pc->tok = u.tok;
+                    pc->ntok = u.ntok;
+                    pc->hk = u.hk;
+                    pc->valid = 1;
+                }
+            }
+            w.advance(p, p1 - p0);
+        }
+        if (lane == 0) {
+            ring[ri] = u;
+            mbar_arrive(b.unit_full(ri));
+        }
+        if (!more) return;
+    }
+}
+
+// The producer warp, all lanes together: Q and the K/V tiles of the planned units.
+template <class T, bool SPARSE>
+__device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, const CUtensorMap* tk,
+                               const CUtensorMap* tv, const PagedBars<T>& b, const PagedShared& sh,
+                               int lane) {
+    const uint32_t sQ = smem_addr(sh.smem), sKV = sQ + T::kOffKV;
+    const PagedUnit* ring = reinterpret_cast<const PagedUnit*>(sh.smem + T::kOffUnits);
     volatile int* abort_flag = sh.abort_flag;
     const int ps = 1 << p.page_shift;
     const int rshift = min(p.page_shift, 7);      // rows of a box: min(page_size, 128)
@@ -330,186 +535,26 @@ __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, con
     const uint64_t pol_first = l2_policy_evict_first(), pol_last = l2_policy_evict_last();
 
     uint32_t it = 0;                  // key tiles loaded by this CTA
-    uint32_t units = 0;
     uint32_t q_used[2] = {0, 0};
-    int qs = 0;
     uint32_t tails = 0, raw_par = 0, raw_last = 0;
 
-    PagedPiece* piece = p.pieces + 2 * blockIdx.x;
-    if (lane < 2) piece[lane].valid = 0;
-    __syncwarp();
-
-    auto publish = [&](const PagedUnit& u) -> bool {
-        const int i = units % T::kUnits;
-        if (units >= (uint32_t)T::kUnits &&
-            !warp_wait(b.unit_empty(i), (units / T::kUnits - 1) & 1, abort_flag))
-            return false;
-        if (lane == 0) {
-            ring[i] = u;
-            mbar_arrive(b.unit_full(i));
-        }
-        ++units;
-        return true;
-    };
-
-    // sparse: the next unit's first 32 list entries and their pages, read while this unit's
-    // tiles stream in
-    bool ahead = false;
-    int ahead_e = -1, ahead_page = -1;
-    long long left = st.length;
-    if (left > 0) {
-        int sb = st.b;
-        PagedSeq s = paged_seq(p, sb);
-        PagedLine line(p, s);
-        // Units of a sequence in order: K/V head by head, and its rows in turn. Sparse
-        // rows go in blocks of st.block tokens, head by head within a block: as a
-        // stretch is about one block long, the CTAs sweep the heads together and
-        // the pages of one head at a time are what L2 has to hold (measured on
-        // 1050 rows of 16 pages of 64, 2 x 15K keys: 718 -> SPARSE_US us).
-        int hk, q, q0 = 0;
-        long long rem = st.offset;
-        if constexpr (SPARSE) {
-            const long long per = (long long)st.block * p.Hkv;
-            const long long i = rem / line.base;
-            rem -= i * line.base;
-            q0 = (int)(i / per) * st.block;
-            const int in = (int)(i - (long long)q0 * p.Hkv), nq = min(st.block, line.m - q0);
-            hk = in / nq;
-            q = q0 + in - hk * nq;
-        } else {
-            const long long head = line.begin(line.m);
-            hk = (int)(rem / head);
-            rem -= hk * head;
-            // the last unit that begins at or before rem
-            int lo = 0, hi = line.m - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (line.begin(mid) <= rem) lo = mid;
-                else hi = mid - 1;
-            }
-            q = lo;
-            rem -= line.begin(q);
-        }
-        for (;;) {
-            const long long ulen = line.unit(q);
-            const long long p0 = rem, p1 = min(ulen, rem + left);
-            PagedUnit u;
-            u.hk = hk;
-            u.tok = s.tok + q * line.U;
-            u.ntok = min(line.U, s.n - q * line.U);
-            u.pos0 = s.len - s.n + q * line.U;
-            u.len = s.len;
-            u.kind = u.ntok > p.tpt ? 2 : 1;
-            u.qs = 0;
-            // key tiles of the whole unit, and of each Q tile
-            int tiles[2];
-            int entries = 0;
-            if constexpr (SPARSE) {
-                // the row's visible pages as runs of up to R keys: (page, first row, keys)
-                const int* row = p.sel + ((size_t)u.tok * p.Hkv + hk) * p.K;
-                const int vis = u.pos0 + 1;   // tokens [0, vis) are visible
-                __syncwarp();
-                int next_e = ahead ? ahead_e : lane < p.K ? __ldg(row + lane) : -1;
-                for (int k0 = 0; k0 < p.K; k0 += 32) {
-                    const int e = next_e;
-                    if (k0 + 32 + lane < p.K) next_e = __ldg(row + k0 + 32 + lane);
-                    else next_e = -1;
-                    const long long t0 = (long long)e << p.page_shift;   // first token of the page
-                    bool ok = e >= 0 && t0 < u.len;
-                    if (!ok && e != -1) atomicOr(&g_attn_status, kDevErrBadIndex);
-                    ok = ok && t0 < vis;
-                    int page = -1, nv = 0;
-                    if (ok) {
-                        page = ahead && k0 == 0
-                                   ? ahead_page
-                                   : __ldg(p.block_table + (size_t)sb * p.max_pages + e);
-                        if (page < 0 || page >= p.num_pages)
-                            atomicOr(&g_attn_status, kDevErrBadIndex);
-                        else
-                            nv = (int)min((long long)ps, vis - t0);
-                    }
-                    const int runs = (nv + R - 1) >> rshift;
-                    int incl = runs;
-#pragma unroll
-                    for (int off = 1; off < 32; off <<= 1) {
-                        const int v = __shfl_up_sync(0xffffffffu, incl, off);
-                        if (lane >= off) incl += v;
-                    }
-                    for (int r = 0; r < runs; ++r)
-                        if (dcheck(entries + incl - runs + r < kPagedListMax))
-                            list[entries + incl - runs + r] =
-                                make_int2(page, (r << rshift << 8) | min(R, nv - (r << rshift)));
-                    entries += __shfl_sync(0xffffffffu, incl, 31);
-                }
-                __syncwarp();
-                tiles[0] = (entries + boxes - 1) / boxes;
-                tiles[1] = 0;
-                u.len = 0x7fffffff;   // the masks say it all
-            } else {
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    int vis = 0;
-                    if (u.ntok > t * p.tpt)
-                        vis = p.causal ? u.pos0 + min((t + 1) * p.tpt, u.ntok) : s.len;
-                    tiles[t] = (max(vis, 0) + 127) >> 7;
-                }
-            }
-            const int all = max(tiles[0], tiles[1]);
-            auto tile_at = [&](long long x) -> int {
-                const long long k = (x - kPagedUnitCost) >> 7;
-                return k < 0 ? 0 : k > all ? all : (int)k;
-            };
-            const int k0 = p0 == 0 ? 0 : tile_at(p0);
-            const int k1 = p1 == ulen ? all : tile_at(p1);
-            const int N = k1 - k0;
-            u.key0 = k0 << 7;
-            if (u.kind == 2) {
-                u.n0 = min(max(tiles[0] - k0, 0), N);
-                u.n1 = min(max(tiles[1] - k0, 0), N);
-            } else {
-                u.n0 = (N + 1) >> 1;
-                u.n1 = N >> 1;
-                u.qs = qs;
-            }
-            u.slot = -1;
-            if (p0 > 0 || p1 < ulen) {
-                u.slot = 2 * blockIdx.x + (p0 > 0 ? 0 : 1);
-                if (lane == 0 && dcheck(u.slot < 2 * kPagedMaxCtas)) {
-                    PagedPiece* x = p.pieces + u.slot;
-                    x->last = p1 == ulen ? 1 : 0;
-                    x->tok = u.tok;
-                    x->ntok = u.ntok;
-                    x->hk = hk;
-                    x->valid = 1;
-                }
-            }
-            if (!publish(u)) goto fail;
-            int ahead_pos = -1;
-            if constexpr (SPARSE) {
-                // the next unit's token and head, if it is in this sequence
-                const bool wrap = q + 1 == min(q0 + st.block, line.m);
-                const bool next_block = wrap && hk + 1 == p.Hkv;
-                ahead = left > p1 - p0 && !(next_block && q + 1 == line.m);
-                if (ahead) {
-                    const int nq = !wrap || next_block ? q + 1 : q0;
-                    const int nh = next_block ? 0 : hk + wrap;
-                    ahead_pos = s.len - s.n + nq;
-                    ahead_e = lane < p.K ? __ldg(p.sel + ((size_t)(s.tok + nq) * p.Hkv + nh) * p.K + lane)
-                                         : -1;
-                }
-            }
-            // the page of entry ahead_e, if the next unit's row can see it
-            auto look_ahead = [&]() {
-                if (SPARSE && ahead && ahead_e >= 0 &&
-                    ((long long)ahead_e << p.page_shift) <= ahead_pos)
-                    ahead_page = __ldg(p.block_table + (size_t)sb * p.max_pages + ahead_e);
-            };
-            if (N == 0) look_ahead();
+    for (uint32_t units = 0;; ++units) {
+        const int ri = units % T::kUnits;
+        if (!warp_wait(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag)) goto fail;
+        {
+            const volatile PagedUnit& u = ring[ri];
+            const int kind = u.kind;
+            if (kind == 0) break;
+            const bool wide = kind == 2;
+            const int hk = u.hk, tok = u.tok, uqs = u.qs, keys_all = u.keys, first = u.key0 >> 7;
+            const int entries = SPARSE ? u.entries : 0;
+            const int N = wide ? max(u.n0, u.n1) : u.n0 + u.n1;
+            const int* table = p.block_table + (size_t)u.seq * p.max_pages;
+            const int2* list = reinterpret_cast<const int2*>(sh.smem + T::kOffList) + ri * kPagedListMax;
             if (N > 0) {
                 // Q: token-major rows of the group's heads
-                const int ntile = u.kind == 2 ? 2 : 1;
-                for (int t = 0; t < ntile; ++t) {
-                    const int slot = u.kind == 2 ? t : qs;
+                for (int t = 0; t < (wide ? 2 : 1); ++t) {
+                    const int slot = wide ? t : uqs;
                     if (q_used[slot] > 0 &&
                         !warp_wait(b.q_empty(slot), (q_used[slot] - 1) & 1, abort_flag))
                         goto fail;
@@ -518,132 +563,106 @@ __device__ void paged_producer(const PagedParams& p, const PagedStretch& st, con
                                               (uint32_t)(T::kPanels * p.tpt * p.G * 128));
                         for (int pn = 0; pn < T::kPanels; ++pn)
                             tma_load_3d(sQ + slot * T::kQBytes + pn * T::kQPanelBytes, tq,
-                                        b.q_full(slot), pn * 64, hk * p.G, u.tok + t * p.tpt);
+                                        b.q_full(slot), pn * 64, hk * p.G, tok + t * p.tpt);
                     }
                     ++q_used[slot];
                 }
-                if (u.kind == 1) qs ^= 1;
-                const uint64_t pol = u.kind == 2 ? pol_last : pol_first;
-                const int* table = p.block_table + (size_t)sb * p.max_pages;
-                // the page, first row and key count of this lane's box of key tile k
-                auto look = [&](int k, int& page, int& y, int& keys) {
-                    if constexpr (SPARSE) {
-                        const int e = k * boxes + bx;
-                        const int2 x = e < entries ? list[e] : make_int2(-1, 0);
-                        page = x.x;
-                        y = x.y >> 8;
-                        keys = x.y & 255;
-                    } else {
-                        const long long key = (long long)k * 128 + bx * R;
-                        const int lp = (int)(key >> p.page_shift);
-                        keys = (int)min(max((long long)s.len - key, 0ll), (long long)R);
-                        y = (int)(key & (ps - 1));
-                        page = keys > 0 && dcheck(lp < p.max_pages) ? __ldg(table + lp) : -1;
-                    }
-                };
-                int page, y, keys;
-                look(k0, page, y, keys);
-                for (int j = 0; j < N; ++j) {
-                    int npage = -1, ny = 0, nkeys = 0;
-                    if (j + 1 < N) look(k0 + j + 1, npage, ny, nkeys);   // ahead of the waits
-                    if (keys > 0 && (page < 0 || page >= p.num_pages)) {
-                        if (panel == 0) atomicOr(&g_attn_status, kDevErrBadIndex);
-                        keys = 0;
-                    }
-                    const int z = keys > 0 ? page * p.Hkv + hk : z_out;
-                    // which of the tile's keys exist, 32 to a word (lanes 0 .. 3)
-                    const int w = lane & 3;
-                    uint32_t word = low_bits(
-                        min(__shfl_sync(0xffffffffu, keys, (32 * w) >> rshift) -
-                                ((32 * w) & (R - 1)), R));
-                    {
-                        const int hi = __shfl_sync(0xffffffffu, keys, ((32 * w) >> rshift) + 1);
-                        if (R == 16) word |= low_bits(min(hi, 16)) << 16;
-                    }
-                    const bool whole = __all_sync(0xffffffffu, word == 0xffffffffu);
-                    const uint32_t pair = it % T::kPairs, round = it / T::kPairs;
-                    const uint32_t sk = 2 * pair, sv = 2 * pair + 1;
-                    if (round > 0 && !warp_wait(b.kv_empty(sk), (round - 1) & 1, abort_flag))
-                        goto fail;
-                    if (lane < 4)
-                        reinterpret_cast<volatile uint32_t*>(
-                            sh.smem + T::kOffMask)[(it % T::kMasks) * 4 + lane] = word;
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(b.kv_full(sk), T::kTileBytes);
-                        mbar_arrive(b.mask_full(it % T::kMasks));
-                    }
-                    __syncwarp();
-                    if (issues)
-                        tma_load_3d_hint(sKV + sk * T::kTileBytes + box_off, tk, b.kv_full(sk),
-                                         panel * 64, y, z, pol);
-                    if (round > 0 && !warp_wait(b.kv_empty(sv), (round - 1) & 1, abort_flag)) {
-                        ++it;   // K is in flight, V is not
+            }
+            const uint64_t pol = wide ? pol_last : pol_first;
+            // the page, first row and key count of this lane's box of key tile k
+            auto look = [&](int k, int& page, int& y, int& keys) {
+                if constexpr (SPARSE) {
+                    const int e = k * boxes + bx;
+                    const int2 x = e < entries ? list[e] : make_int2(-1, 0);
+                    page = x.x;
+                    y = x.y >> 8;
+                    keys = x.y & 255;
+                } else {
+                    const long long key = (long long)k * 128 + bx * R;
+                    const int lp = (int)(key >> p.page_shift);
+                    keys = (int)min(max((long long)keys_all - key, 0ll), (long long)R);
+                    y = (int)(key & (ps - 1));
+                    page = keys > 0 && dcheck(lp < p.max_pages) ? __ldg(table + lp) : -1;
+                }
+            };
+            int page = -1, y = 0, keys = 0;
+            if (N > 0) look(first, page, y, keys);
+            for (int j = 0; j < N; ++j) {
+                int npage = -1, ny = 0, nkeys = 0;
+                if (j + 1 < N) look(first + j + 1, npage, ny, nkeys);   // ahead of the waits
+                if (keys > 0 && (page < 0 || page >= p.num_pages)) {
+                    if (panel == 0) atomicOr(&g_attn_status, kDevErrBadIndex);
+                    keys = 0;
+                }
+                const int z = keys > 0 ? page * p.Hkv + hk : z_out;
+                // which of the tile's keys exist, 32 to a word (lanes 0 .. 3)
+                const int wi = lane & 3;
+                uint32_t word =
+                    low_bits(min(__shfl_sync(0xffffffffu, keys, (32 * wi) >> rshift) -
+                                     ((32 * wi) & (R - 1)), R));
+                {
+                    const int hi = __shfl_sync(0xffffffffu, keys, ((32 * wi) >> rshift) + 1);
+                    if (R == 16) word |= low_bits(min(hi, 16)) << 16;
+                }
+                const bool whole = __all_sync(0xffffffffu, word == 0xffffffffu);
+                const uint32_t pair = it % T::kPairs, round = it / T::kPairs;
+                const uint32_t sk = 2 * pair, sv = 2 * pair + 1;
+                if (round > 0 && !warp_wait(b.kv_empty(sk), (round - 1) & 1, abort_flag)) goto fail;
+                if (lane < 4)
+                    reinterpret_cast<volatile uint32_t*>(
+                        sh.smem + T::kOffMask)[(it % T::kMasks) * 4 + lane] = word;
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(b.kv_full(sk), T::kTileBytes);
+                    mbar_arrive(b.mask_full(it % T::kMasks));
+                }
+                __syncwarp();
+                if (issues)
+                    tma_load_3d_hint(sKV + sk * T::kTileBytes + box_off, tk, b.kv_full(sk),
+                                     panel * 64, y, z, pol);
+                if (round > 0 && !warp_wait(b.kv_empty(sv), (round - 1) & 1, abort_flag)) {
+                    ++it;   // K is in flight, V is not
+                    raw_last |= 1u << (8 + pair);
+                    goto fail;
+                }
+                uint32_t vbar = b.kv_full(sv);
+                if (!whole) {   // rows without a key must be zeroed before P V
+                    const uint32_t i = tails & 1;
+                    if (tails >= 2 &&
+                        !warp_wait(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) {
+                        ++it;
                         raw_last |= 1u << (8 + pair);
                         goto fail;
                     }
-                    uint32_t vbar = b.kv_full(sv);
-                    if (!whole) {   // rows without a key must be zeroed before P V
-                        const uint32_t i = tails & 1;
-                        if (tails >= 2 &&
-                            !warp_wait(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) {
-                            ++it;
-                            raw_last |= 1u << (8 + pair);
-                            goto fail;
-                        }
-                        vbar = b.v_raw(pair);
-                        if (lane == 0) {
-                            reinterpret_cast<volatile int*>(sh.tail_info)[i] =
-                                (int)(pair | ((it % T::kMasks) << 8));
-                            mbar_arrive_expect_tx(vbar, T::kTileBytes);
-                            mbar_arrive(b.tail_full(i));
-                        }
-                        ++tails;
-                        raw_par ^= 1u << pair;
-                        raw_last |= 1u << pair;
-                    } else {
-                        if (lane == 0) mbar_arrive_expect_tx(vbar, T::kTileBytes);
-                        raw_last &= ~(1u << pair);
+                    vbar = b.v_raw(pair);
+                    if (lane == 0) {
+                        reinterpret_cast<volatile int*>(sh.tail_info)[i] =
+                            (int)(pair | ((it % T::kMasks) << 8));
+                        mbar_arrive_expect_tx(vbar, T::kTileBytes);
+                        mbar_arrive(b.tail_full(i));
                     }
-                    if (T::kIssuers > 1 && lane == 0) mbar_arrive(b.v_given(it % T::kMasks));
-                    __syncwarp();
-                    if (issues)
-                        tma_load_3d_hint(sKV + sv * T::kTileBytes + box_off, tv, vbar, panel * 64,
-                                         y, z, pol);
-                    ++it;
-                    if (j == 0) look_ahead();
-                    page = npage;
-                    y = ny;
-                    keys = nkeys;
-                }
-            }
-            left -= p1 - p0;
-            rem = 0;
-            if (left <= 0) break;
-            // the next unit
-            if (++q == (SPARSE ? min(q0 + st.block, line.m) : line.m)) {
-                if (++hk < p.Hkv) {
-                    q = q0;
+                    ++tails;
+                    raw_par ^= 1u << pair;
+                    raw_last |= 1u << pair;
                 } else {
-                    hk = 0;
-                    q0 = q;
-                    if (q == line.m) {
-                        do {
-                            if (++sb >= p.B) break;
-                            s = paged_seq(p, sb);
-                        } while (s.n == 0);
-                        if (sb >= p.B) break;
-                        line = PagedLine(p, s);
-                        q = q0 = 0;
-                    }
+                    if (lane == 0) mbar_arrive_expect_tx(vbar, T::kTileBytes);
+                    raw_last &= ~(1u << pair);
                 }
+                if (T::kIssuers > 1 && lane == 0) mbar_arrive(b.v_given(it % T::kMasks));
+                __syncwarp();
+                if (issues)
+                    tma_load_3d_hint(sKV + sv * T::kTileBytes + box_off, tv, vbar, panel * 64, y, z,
+                                     pol);
+                ++it;
+                page = npage;
+                y = ny;
+                keys = nkeys;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b.unit_empty(ri));   // the list is read
         }
     }
     {
-        PagedUnit u;
-        u.kind = 0;
-        if (!publish(u)) goto fail;
         const uint32_t i = tails & 1;
         if (tails >= 2 && !warp_wait(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) goto fail;
         if (lane == 0) {
@@ -968,10 +987,10 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
                 ml[r].x = m_ref;
                 ml[r].y = l;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b.ml_full());
+                if (lane == 0) mbar_arrive(b.ml_full(0));
             } else {
                 // group 1 has waited for its own o_final by then
-                if (!warp_wait(b.ml_full(), ml_cnt & 1, abort_flag)) return;
+                if (!warp_wait(b.ml_full(0), ml_cnt & 1, abort_flag)) return;
                 if (!warp_wait(b.o_final(1), o_used[1] & 1, abort_flag)) return;
                 const float m1 = ml[r].x, l1 = ml[r].y;
                 const float m = fmaxf(m_ref, m1);
@@ -1092,16 +1111,16 @@ __device__ __forceinline__ void paged_init(const PagedBars<T>& b, const PagedSha
     }
     for (int i = 0; i < T::kUnits; ++i) {
         mbar_init(b.unit_full(i), 1);
-        mbar_init(b.unit_empty(i), T::kIssuers + 8);   // the issuers and 8 softmax warps
+        mbar_init(b.unit_empty(i), T::kIssuers + 9);   // the issuers, producer, 8 softmax warps
     }
-    mbar_init(b.ml_full(), 4);
+    for (int t = 0; t < 2; ++t) mbar_init(b.ml_full(t), 4);
     mbar_init(b.drain(), T::kIssuers);
     *sh.abort_flag = 0;
     fence_mbar_init();
 }
 
 template <int D, bool SPARSE>
-__global__ void __launch_bounds__(kPagedThreads, 1)
+__global__ void __launch_bounds__(PagedTraits<D>::kThreads, 1)
     attn_paged_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
                             const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
@@ -1118,6 +1137,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     sh.tail_info = reinterpret_cast<int*>(tmem_holder + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    // the merge may be set up as soon as SMs have room; it waits for this grid's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) paged_init<T>(b, sh);
     if (warp == 8 && lane == 0) {
         tma_prefetch_desc(&tm_q);
@@ -1129,7 +1150,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         tmem_relinquish();
     }
     // the staging area is free until the first epilogue
-    const PagedStretch st = paged_schedule(p, reinterpret_cast<long long*>(smem + T::kOffStage));
+    const PagedStretch st =
+        paged_schedule<T::kThreads>(p, reinterpret_cast<long long*>(smem + T::kOffStage));
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -1141,11 +1163,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     } else {
         regs_decrease<T::kOtherRegs>();
         if (warp == 8)
-            paged_producer<T, SPARSE>(p, st, &tm_q, &tm_k, &tm_v, b, sh, lane);
+            paged_producer<T, SPARSE>(p, &tm_q, &tm_k, &tm_v, b, sh, lane);
         else if (warp == 9) {
             if (lane == 0) paged_mma<D>(tbase, b, sh);
         } else if (warp == 10)
             paged_tail<T>(b, sh, lane);
+        else
+            paged_planner<T, SPARSE>(p, st, b, sh, lane);
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -1167,45 +1191,51 @@ template <int D>
 __global__ void __launch_bounds__(kPagedMergeThreads)
     attn_paged_merge_kernel(const PagedParams p, int ctas) {
     constexpr int kPerRow = D / 4, kRows = kPagedMergeThreads / kPerRow;
+    // launched while the attention kernel still runs; nothing of it is read before it is over
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x;
     const PagedPiece first = p.pieces[2 * c + 1];
     if (!first.valid) return;
-    const int R = blockIdx.y * kRows + threadIdx.x / kPerRow;   // row of the unit's 256
-    const int t = R >> 7, r = R & 127, col = threadIdx.x % kPerRow;
-    if (r >= min(max(first.ntok - t * p.tpt, 0), p.tpt) * p.G) return;
     constexpr float kLog2e = 1.4426950408889634f;
-    float M = -INFINITY, W = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    int slot = 2 * c + 1;
-    for (;;) {
-        const size_t row = (size_t)slot * 256 + R;
-        const float ls = p.part_lse[row];
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * col);
-        const PagedPiece pc = p.pieces[slot];
-        const float mn = fmaxf(M, ls);
-        if (mn != -INFINITY) {
-            // NaN partials stay NaN: fmaxf drops them from the maximum, not from W
-            const float a = fast_exp2((M - mn) * kLog2e), w = fast_exp2((ls - mn) * kLog2e);
-            W = W * a + w;
-            acc.x = acc.x * a + w * x.x;
-            acc.y = acc.y * a + w * x.y;
-            acc.z = acc.z * a + w * x.z;
-            acc.w = acc.w * a + w * x.w;
-            M = mn;
-        } else if (!(ls == -INFINITY)) {
-            W = ls;   // NaN and nothing before it
+    const int col = threadIdx.x % kPerRow;
+    // R: row of the unit's (at most) 256
+    for (int R = blockIdx.y * kRows + threadIdx.x / kPerRow; R < 256; R += gridDim.y * kRows) {
+        const int t = R >> 7, r = R & 127;
+        if (r >= min(max(first.ntok - t * p.tpt, 0), p.tpt) * p.G) continue;
+        float M = -INFINITY, W = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        int slot = 2 * c + 1;
+        for (;;) {
+            const size_t row = (size_t)slot * 256 + R;
+            const float ls = p.part_lse[row];
+            const float4 x = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * col);
+            const int last = p.pieces[slot].last;
+            const float mn = fmaxf(M, ls);
+            if (mn != -INFINITY) {
+                // NaN partials stay NaN: fmaxf drops them from the maximum, not from W
+                const float a = fast_exp2((M - mn) * kLog2e), w = fast_exp2((ls - mn) * kLog2e);
+                W = W * a + w;
+                acc.x = acc.x * a + w * x.x;
+                acc.y = acc.y * a + w * x.y;
+                acc.z = acc.z * a + w * x.z;
+                acc.w = acc.w * a + w * x.w;
+                M = mn;
+            } else if (!(ls == -INFINITY)) {
+                W = ls;   // NaN and nothing before it
+            }
+            if (last) break;
+            slot = (slot | 1) + 1;   // the next CTA's continuing piece
+            if (slot >= 2 * ctas || !p.pieces[slot].valid) break;
         }
-        if (pc.last) break;
-        slot = (slot | 1) + 1;   // the next CTA's continuing piece
-        if (slot >= 2 * ctas || !p.pieces[slot].valid) break;
+        const int tk = r / p.G;
+        const size_t row =
+            (size_t)(first.tok + t * p.tpt + tk) * p.Hq + first.hk * p.G + (r - tk * p.G);
+        if (!dcheck(row < (size_t)p.T * p.Hq)) continue;
+        const float inv = W != 0.f ? 1.0f / W : 0.f;
+        *reinterpret_cast<uint2*>(p.o + row * D + 4 * col) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (col == 0) p.lse[row] = W != 0.f ? M + logf(W) : -INFINITY;
     }
-    const int tk = r / p.G;
-    const size_t row = (size_t)(first.tok + t * p.tpt + tk) * p.Hq + first.hk * p.G + (r - tk * p.G);
-    if (!dcheck(row < (size_t)p.T * p.Hq)) return;
-    const float inv = W != 0.f ? 1.0f / W : 0.f;
-    *reinterpret_cast<uint2*>(p.o + row * D + 4 * col) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (col == 0) p.lse[row] = W != 0.f ? M + logf(W) : -INFINITY;
 }
 
 }  // namespace eattn

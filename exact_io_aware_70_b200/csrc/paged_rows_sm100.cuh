@@ -18,7 +18,8 @@
 //   * P goes to shared memory (bf16, 128-byte swizzle) as the second operand;
 //     V, stored [keys][D], is the first operand as it lies (M-major).
 // The two softmax groups take alternate key tiles, each with its own issuing
-// thread, so neither waits for the other; group 0 joins the results.
+// thread, so neither waits for the other; they take turns at joining their results
+// (group 0 when it alone had a tile).
 #pragma once
 
 #include <cfloat>
@@ -67,6 +68,24 @@ __device__ __forceinline__ float warp_sum16(float (&v)[16], int lane) {
         }
     }
     return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// 8 columns of this warp's 32 tensor-memory lanes; the wait takes in two such loads.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld8(uint32_t (&a)[8], uint32_t (&b)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]),
+                   "+r"(a[6]), "+r"(a[7]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]),
+                   "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+                 :
+                 : "memory");
 }
 
 // N consecutive columns of this warp's 32 tensor-memory lanes
@@ -183,17 +202,17 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
     const uint32_t lane_off = uint32_t(quarter * 32) << 16;
     const uint32_t tS = tbase + lane_off + (t ? T::kColS1 : T::kColS0);
     const uint32_t tO = tbase + lane_off + (t ? T::kColO1 : T::kColO0);
-    const uint32_t tO1 = tbase + lane_off + T::kColO1;
+    const uint32_t tOther = tbase + lane_off + (t ? T::kColO0 : T::kColO1);
     volatile int* abort_flag = sh.abort_flag;
     const PagedUnit* ring = reinterpret_cast<const PagedUnit*>(sh.smem + T::kOffUnits);
     const volatile uint32_t* masks =
         reinterpret_cast<const volatile uint32_t*>(sh.smem + T::kOffMask);
-    // per row: group 1's (m, l) and group 0's weights (apart: group 1 may be a unit ahead);
+    // per row: (m, l) for the joining group, and each group's weights as it joins;
     // per group: the negated reference maximum (the lowest float before the
     // first key: every score is far above it), the factor of a rescaling, a word per warp
     float2* ml = reinterpret_cast<float2*>(sh.smem + T::kOffMl);
-    float2* weight = ml + N;
-    float* minus_ref = reinterpret_cast<float*>(sh.smem + T::kOffMl + 2 * N * 8) + t * 6 * N;
+    float2* weight = ml + (1 + t) * N;
+    float* minus_ref = reinterpret_cast<float*>(sh.smem + T::kOffMl + 3 * N * 8) + t * 6 * N;
     float* alpha = minus_ref + N;
     float* red = alpha + N;
     // where key r of row c goes in P: 128-byte rows of 64 keys, 16-byte pieces swizzled by row
@@ -359,26 +378,28 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
             }
         }
         const bool both = un[1] > 0;
-        if (t == 1) {
+        const int joiner = both ? (int)(units & 1) : 0;
+        if (t != joiner) {
             if (both) {
                 if (r < N) ml[r] = make_float2(m, sum);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b.ml_full());
+                if (lane == 0) mbar_arrive(b.ml_full(joiner));
             }
         } else {
             if (both) {
-                const bool ok = warp_wait(b.ml_full(), ml_cnt & 1, abort_flag) &&
-                                warp_wait(b.o_final(1), o_used[1] & 1, abort_flag);
-                if (group_any(0, !ok)) return;
+                // the other group has waited for its own o_final by then
+                const bool ok = warp_wait(b.ml_full(t), ml_cnt & 1, abort_flag) &&
+                                warp_wait(b.o_final(t ^ 1), o_used[t ^ 1] & 1, abort_flag);
+                if (group_any(t, !ok)) return;
                 ++ml_cnt;
             }
             if (r < N && r < rows) {
                 float w0 = n > 0 ? 1.f : 0.f, w1 = 0.f;
                 if (both) {
                     const float2 o = ml[r];
-                    const float mn = fmaxf(m, o.x), mb = mn == -INFINITY ? 0.f : mn;
-                    w0 = fast_exp2(m - mb);
-                    w1 = fast_exp2(o.x - mb);
+                    const float mn = fmaxf(m, o.x);
+                    w0 = fast_exp2(m - mn);
+                    w1 = fast_exp2(o.x - mn);
                     sum = sum * w0 + o.y * w1;
                     m = mn;
                 }
@@ -393,48 +414,45 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
                     p.part_lse[(size_t)slot * 256 + r] = lse;
                 }
             }
-            group_sync(0);
+            group_sync(t);
             tc_fence_after_sync();
             const int dim = D == 128 ? r : quarter * 16 + lane;
             const bool has_dim = D == 128 || lane < 16;
-            size_t row = slot < 0 ? (size_t)tok0 * p.Hq + hk * p.G : (size_t)slot * 256;
+            const size_t row0 = slot < 0 ? (size_t)tok0 * p.Hq + hk * p.G : (size_t)slot * 256;
+            uint16_t* dst = p.o + row0 * D + dim;
+            float* part = p.part_o + row0 * D + dim;
+            const size_t skip = (size_t)(p.Hq - p.G) * D;    // to the group's heads of the next token
             int head = 0;
 #pragma unroll 1
-            for (int c0 = 0; c0 < rows; c0 += 16) {
-                uint32_t o0[16], o1[16];
-                if (n > 0) {
-                    tmem_ld16(tO + c0, o0);
-                    tmem_wait_ld16(o0);
-                }
-                if (both) {
-                    tmem_ld16(tO1 + c0, o1);
-                    tmem_wait_ld16(o1);
-                }
+            for (int c0 = 0; c0 < rows; c0 += 8) {
+                uint32_t o0[8], o1[8];
+                tmem_ld8(tO + c0, o0);
+                tmem_ld8(tOther + c0, o1);
+                tmem_wait_ld8(o0, o1);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    if (c0 + c < rows) {
-                        const float2 w = weight[c0 + c];
-                        float v = n > 0 ? __uint_as_float(o0[c]) * w.x : 0.f;
-                        if (both) v = fmaf(__uint_as_float(o1[c]), w.y, v);
-                        if (slot < 0) {
-                            if (has_dim && dcheck(row < (size_t)p.T * p.Hq))
-                                p.o[row * D + dim] = (uint16_t)pack_bf16x2(v, 0.f);
-                            ++row;
-                            if (++head == p.G) {     // the group's heads of the next token
-                                head = 0;
-                                row += p.Hq - p.G;
-                            }
-                        } else {
-                            if (has_dim && dcheck(row < (size_t)512 * kPagedMaxCtas))
-                                p.part_o[row * D + dim] = v;
-                            ++row;
+                for (int c = 0; c < 8; ++c) {
+                    if (c0 + c >= rows) break;
+                    const float2 w = weight[c0 + c];
+                    float v = n > 0 ? __uint_as_float(o0[c]) * w.x : 0.f;
+                    if (both) v = fmaf(__uint_as_float(o1[c]), w.y, v);
+                    if (slot < 0) {
+                        if (has_dim && dcheck(dst < p.o + (size_t)p.T * p.Hq * D))
+                            *dst = (uint16_t)pack_bf16x2(v, 0.f);
+                        dst += D;
+                        if (++head == p.G) {
+                            head = 0;
+                            dst += skip;
                         }
+                    } else {
+                        if (has_dim && dcheck(part < p.part_o + (size_t)512 * kPagedMaxCtas * D))
+                            *part = v;
+                        part += D;
                     }
                 }
             }
-            group_sync(0);       // the weights are read
-            if (n > 0) softmax_arrive<true>(b.o_free(0), lane);
-            if (both) softmax_arrive<true>(b.o_free(1), lane);
+            group_sync(t);       // the weights are read
+            if (n > 0) softmax_arrive<true>(b.o_free(t), lane);
+            if (both) softmax_arrive<true>(b.o_free(t ^ 1), lane);
         }
         for (int k = 0; k < 2; ++k)
             if (un[k] > 0) ++o_used[k];
@@ -443,7 +461,7 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
 
 // ---------------------------------------------------------------- kernel --
 template <int D, int N, bool SPARSE>
-__global__ void __launch_bounds__(kPagedThreads, 1)
+__global__ void __launch_bounds__(PagedTraits<D, N>::kThreads, 1)
     attn_paged_rows_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
                                  const __grid_constant__ CUtensorMap tm_k,
                                  const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
@@ -460,6 +478,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     sh.tail_info = reinterpret_cast<int*>(tmem_holder + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge, as there
     if (threadIdx.x == 0) paged_init<T>(b, sh);
     if (warp == 8 && lane == 0) {
         tma_prefetch_desc(&tm_q);
@@ -471,11 +490,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         tmem_relinquish();
     }
     // Q rows that no copy ever writes are zeros, so their columns stay finite
-    for (int i = threadIdx.x; i < 2 * T::kQBytes / 16; i += kPagedThreads)
+    for (int i = threadIdx.x; i < 2 * T::kQBytes / 16; i += T::kThreads)
         reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     fence_async_shared();
     // P's area is free until the first tile
-    const PagedStretch st = paged_schedule(p, reinterpret_cast<long long*>(smem + T::kOffStage));
+    const PagedStretch st =
+        paged_schedule<T::kThreads>(p, reinterpret_cast<long long*>(smem + T::kOffStage));
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -484,11 +504,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     if (warp < 8)
         rows_softmax<D, N>(p, tbase, b, sh, warp, lane);
     else if (warp == 8)
-        paged_producer<T, SPARSE>(p, st, &tm_q, &tm_k, &tm_v, b, sh, lane);
+        paged_producer<T, SPARSE>(p, &tm_q, &tm_k, &tm_v, b, sh, lane);
     else if (warp == 9 || warp == 11) {
         if (lane == 0) rows_mma<D, N>(tbase, b, sh, warp == 9 ? 0 : 1);
-    } else
+    } else if (warp == 10)
         paged_tail<T>(b, sh, lane);
+    else
+        paged_planner<T, SPARSE>(p, st, b, sh, lane);
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();

@@ -403,7 +403,7 @@ attn_status_t attn_page_select(const void *q, const void *k_bounds, const int *b
  *        skipped, pages past the token's position hold no visible key, entries
  *        past the sequence's last page are skipped and reported. A page listed
  *        twice counts twice.
- *   num_sel >= 1, num_sel * max(1, page_size / 128) <= 1024.
+ *   num_sel >= 1, num_sel * max(1, page_size / 128) <= 480.
  */
 attn_status_t attn_sparse_paged(const void *q, const void *k_cache, const void *v_cache,
                                 const int *block_table, const int *cu_q, const int *seq_lens,

@@ -73,7 +73,7 @@ SPARSE = dict(q=P, kc=P, vc=P, table=P, cu=P, seq=P, sel=P, o=P, lse=P, B=2, T=4
 
 @pytest.mark.parametrize("kw,code", [
     (dict(sel=None), INV), (dict(q=None), INV), (dict(sel=P + 2), ALI), (dict(K=0), INV),
-    (dict(K=1025), UNS), (dict(K=129, page_size=1024), UNS), (dict(ws_bytes=0), INV),
+    (dict(K=481), UNS), (dict(K=61, page_size=1024), UNS), (dict(ws_bytes=0), INV),
     (dict(o=P + 2), ALI), (dict(Hq=9), INV), (dict(scale=-1.0), INV),
 ])
 def test_sparse_refusals(kw, code):
