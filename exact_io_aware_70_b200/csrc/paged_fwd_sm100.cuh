@@ -89,8 +89,10 @@ struct PagedTraits {
     // the mask ring is longer than the K/V ring by the tiles that units planned ahead can have
     // without any work for one of the groups (kUnits, one tile each)
     static constexpr int kMasks = 2 * kPairs + 2 * kUnits;
-    static constexpr int kThreads = N ? 416 : 384;       // a 13th warp plans; else warp 11 does
-    static constexpr int kPlanner = N ? 12 : 11;
+    // N > 0: warp 12 plans and warp 13 loads V (one warp for both takes 1.1 us per key tile to
+    // issue its copies: too long where K and V come from L2); else warp 11 plans
+    static constexpr int kThreads = N ? 448 : 384;
+    static constexpr int kLoaders = N ? 2 : 1;
     static constexpr int kQRows = N ? N : 128;
     static constexpr int kQPanelBytes = kQRows * 128;
     static constexpr int kQBytes = kPanels * kQPanelBytes;    // one Q slot (of two)
@@ -171,6 +173,29 @@ struct PagedUnit {
     int pad[2];
 };
 static_assert(sizeof(PagedUnit) == 64, "unit record");
+
+// Waits of the roles. Where few registers are live (N > 0) the part that actually waits is
+// one function for all of them: some thirty copies of it, inlined, kept the SM's
+// instruction cache (shared by roles that run different code at the same time) from
+// holding their loops.
+__device__ __noinline__ bool paged_wait_slow(uint32_t bar, uint32_t parity,
+                                             volatile int* abort_flag) {
+    return mbar_wait_limit(bar, parity, abort_flag, &g_attn_status, kWaitLimitNs);
+}
+template <class T>
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity,
+                                           volatile int* abort_flag) {
+    if constexpr (T::kN == 0) return mbar_wait(bar, parity, abort_flag, &g_attn_status);
+    if (mbar_test(bar, parity)) return true;
+    return paged_wait_slow(bar, parity, abort_flag);
+}
+// by a whole warp; the outcome is the same in all lanes
+template <class T>
+__device__ __forceinline__ bool paged_warp_wait(uint32_t bar, uint32_t parity,
+                                                volatile int* abort_flag) {
+    const bool ok = paged_wait<T>(bar, parity, abort_flag);
+    return __all_sync(0xffffffffu, ok);
+}
 
 // ------------------------------------------------------------- schedule --
 struct PagedSeq {
@@ -303,7 +328,8 @@ __device__ __forceinline__ uint32_t low_bits(int n) {   // n clamped to 0 .. 32
 struct PagedShared {
     uint8_t* smem;
     volatile int* abort_flag;
-    int* tail_info;   // [2]
+    int* tail_info;        // [2]: the pair
+    uint32_t* tail_mask;   // [2][4]: its keys
 };
 
 // 3-D tile load with an L2 policy, one box per calling lane.
@@ -409,7 +435,7 @@ __device__ void paged_planner(const PagedParams& p, const PagedStretch& st, cons
             if (visible(ahead_e)) ahead_page = page_of(ahead_e);
         }
         if (units >= (uint32_t)T::kUnits &&
-            !warp_wait(b.unit_empty(ri), (units / T::kUnits - 1) & 1, sh.abort_flag))
+            !paged_warp_wait<T>(b.unit_empty(ri), (units / T::kUnits - 1) & 1, sh.abort_flag))
             return;
         if (more) {
             const long long ulen = w.line.unit(w.q);
@@ -515,8 +541,9 @@ __device__ void paged_planner(const PagedParams& p, const PagedStretch& st, cons
     }
 }
 
-// The producer warp, all lanes together: Q and the K/V tiles of the planned units.
-template <class T, bool SPARSE>
+// A producer warp, all lanes together: Q and the K/V tiles of the planned units. K and V:
+// which of the two it loads (Q and the masks go with K).
+template <class T, bool SPARSE, bool K, bool V>
 __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, const CUtensorMap* tk,
                                const CUtensorMap* tv, const PagedBars<T>& b, const PagedShared& sh,
                                int lane) {
@@ -540,7 +567,7 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
 
     for (uint32_t units = 0;; ++units) {
         const int ri = units % T::kUnits;
-        if (!warp_wait(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag)) goto fail;
+        if (!paged_warp_wait<T>(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag)) goto fail;
         {
             const volatile PagedUnit& u = ring[ri];
             const int kind = u.kind;
@@ -551,12 +578,12 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
             const int N = wide ? max(u.n0, u.n1) : u.n0 + u.n1;
             const int* table = p.block_table + (size_t)u.seq * p.max_pages;
             const int2* list = reinterpret_cast<const int2*>(sh.smem + T::kOffList) + ri * kPagedListMax;
-            if (N > 0) {
+            if (K && N > 0) {
                 // Q: token-major rows of the group's heads
                 for (int t = 0; t < (wide ? 2 : 1); ++t) {
                     const int slot = wide ? t : uqs;
                     if (q_used[slot] > 0 &&
-                        !warp_wait(b.q_empty(slot), (q_used[slot] - 1) & 1, abort_flag))
+                        !paged_warp_wait<T>(b.q_empty(slot), (q_used[slot] - 1) & 1, abort_flag))
                         goto fail;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(b.q_full(slot),
@@ -607,52 +634,58 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
                 const bool whole = __all_sync(0xffffffffu, word == 0xffffffffu);
                 const uint32_t pair = it % T::kPairs, round = it / T::kPairs;
                 const uint32_t sk = 2 * pair, sv = 2 * pair + 1;
-                if (round > 0 && !warp_wait(b.kv_empty(sk), (round - 1) & 1, abort_flag)) goto fail;
-                if (lane < 4)
-                    reinterpret_cast<volatile uint32_t*>(
-                        sh.smem + T::kOffMask)[(it % T::kMasks) * 4 + lane] = word;
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(b.kv_full(sk), T::kTileBytes);
-                    mbar_arrive(b.mask_full(it % T::kMasks));
+                if constexpr (K) {
+                    if (round > 0 && !paged_warp_wait<T>(b.kv_empty(sk), (round - 1) & 1, abort_flag))
+                        goto fail;
+                    if (lane < 4)
+                        reinterpret_cast<volatile uint32_t*>(
+                            sh.smem + T::kOffMask)[(it % T::kMasks) * 4 + lane] = word;
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(b.kv_full(sk), T::kTileBytes);
+                        mbar_arrive(b.mask_full(it % T::kMasks));
+                    }
+                    __syncwarp();
+                    if (issues)
+                        tma_load_3d_hint(sKV + sk * T::kTileBytes + box_off, tk, b.kv_full(sk),
+                                         panel * 64, y, z, pol);
                 }
-                __syncwarp();
-                if (issues)
-                    tma_load_3d_hint(sKV + sk * T::kTileBytes + box_off, tk, b.kv_full(sk),
-                                     panel * 64, y, z, pol);
-                if (round > 0 && !warp_wait(b.kv_empty(sv), (round - 1) & 1, abort_flag)) {
-                    ++it;   // K is in flight, V is not
-                    raw_last |= 1u << (8 + pair);
-                    goto fail;
-                }
-                uint32_t vbar = b.kv_full(sv);
-                if (!whole) {   // rows without a key must be zeroed before P V
-                    const uint32_t i = tails & 1;
-                    if (tails >= 2 &&
-                        !warp_wait(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) {
-                        ++it;
+                if constexpr (V) {
+                    if (round > 0 && !paged_warp_wait<T>(b.kv_empty(sv), (round - 1) & 1, abort_flag)) {
+                        ++it;   // this tile's V is not in flight
                         raw_last |= 1u << (8 + pair);
                         goto fail;
                     }
-                    vbar = b.v_raw(pair);
-                    if (lane == 0) {
-                        reinterpret_cast<volatile int*>(sh.tail_info)[i] =
-                            (int)(pair | ((it % T::kMasks) << 8));
-                        mbar_arrive_expect_tx(vbar, T::kTileBytes);
-                        mbar_arrive(b.tail_full(i));
+                    uint32_t vbar = b.kv_full(sv);
+                    if (!whole) {   // rows without a key must be zeroed before P V
+                        const uint32_t i = tails & 1;
+                        if (tails >= 2 &&
+                            !paged_warp_wait<T>(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) {
+                            ++it;
+                            raw_last |= 1u << (8 + pair);
+                            goto fail;
+                        }
+                        vbar = b.v_raw(pair);
+                        if (lane < 4) reinterpret_cast<volatile uint32_t*>(sh.tail_mask)[4 * i + lane] = word;
+                        __syncwarp();
+                        if (lane == 0) {
+                            reinterpret_cast<volatile int*>(sh.tail_info)[i] = (int)pair;
+                            mbar_arrive_expect_tx(vbar, T::kTileBytes);
+                            mbar_arrive(b.tail_full(i));
+                        }
+                        ++tails;
+                        raw_par ^= 1u << pair;
+                        raw_last |= 1u << pair;
+                    } else {
+                        if (lane == 0) mbar_arrive_expect_tx(vbar, T::kTileBytes);
+                        raw_last &= ~(1u << pair);
                     }
-                    ++tails;
-                    raw_par ^= 1u << pair;
-                    raw_last |= 1u << pair;
-                } else {
-                    if (lane == 0) mbar_arrive_expect_tx(vbar, T::kTileBytes);
-                    raw_last &= ~(1u << pair);
+                    if (T::kIssuers > 1 && lane == 0) mbar_arrive(b.v_given(it % T::kMasks));
+                    __syncwarp();
+                    if (issues)
+                        tma_load_3d_hint(sKV + sv * T::kTileBytes + box_off, tv, vbar, panel * 64, y,
+                                         z, pol);
                 }
-                if (T::kIssuers > 1 && lane == 0) mbar_arrive(b.v_given(it % T::kMasks));
-                __syncwarp();
-                if (issues)
-                    tma_load_3d_hint(sKV + sv * T::kTileBytes + box_off, tv, vbar, panel * 64, y, z,
-                                     pol);
                 ++it;
                 page = npage;
                 y = ny;
@@ -662,9 +695,9 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
             if (lane == 0) mbar_arrive(b.unit_empty(ri));   // the list is read
         }
     }
-    {
+    if (V) {
         const uint32_t i = tails & 1;
-        if (tails >= 2 && !warp_wait(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) goto fail;
+        if (tails >= 2 && !paged_warp_wait<T>(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) goto fail;
         if (lane == 0) {
             reinterpret_cast<volatile int*>(sh.tail_info)[i] = -1;
             mbar_arrive(b.tail_full(i));
@@ -679,17 +712,17 @@ fail:
         const uint32_t first = it > (uint32_t)T::kPairs ? it - T::kPairs : 0;
         for (uint32_t i = first; i < it; ++i) {
             const uint32_t pair = i % T::kPairs, par = (i / T::kPairs) & 1;
-            mbar_wait(b.kv_full(2 * pair), par, &no_abort, &g_attn_status);
+            if (K) paged_wait<T>(b.kv_full(2 * pair), par, &no_abort);
             const bool no_v = i + 1 == it && ((raw_last >> (8 + pair)) & 1);
-            if (no_v) continue;
+            if (!V || no_v) continue;
             if ((raw_last >> pair) & 1)
-                mbar_wait(b.v_raw(pair), ((raw_par >> pair) & 1) ^ 1, &no_abort, &g_attn_status);
+                paged_wait<T>(b.v_raw(pair), ((raw_par >> pair) & 1) ^ 1, &no_abort);
             else
-                mbar_wait(b.kv_full(2 * pair + 1), par, &no_abort, &g_attn_status);
+                paged_wait<T>(b.kv_full(2 * pair + 1), par, &no_abort);
         }
         for (int i = 0; i < 2; ++i)
-            if (q_used[i] > 0)
-                mbar_wait(b.q_full(i), (q_used[i] - 1) & 1, &no_abort, &g_attn_status);
+            if (K && q_used[i] > 0)
+                paged_wait<T>(b.q_full(i), (q_used[i] - 1) & 1, &no_abort);
     }
     __syncwarp();
 }
@@ -700,14 +733,13 @@ __device__ void paged_tail(const PagedBars<T>& b, const PagedShared& sh, int lan
     const uint32_t sKV = smem_addr(sh.smem) + T::kOffKV;
     uint32_t par = 0;
     for (uint32_t i = 0;; ++i) {
-        if (!warp_wait(b.tail_full(i & 1), (i >> 1) & 1, sh.abort_flag)) return;
+        if (!paged_warp_wait<T>(b.tail_full(i & 1), (i >> 1) & 1, sh.abort_flag)) return;
         const int info = reinterpret_cast<volatile int*>(sh.tail_info)[i & 1];
         if (info < 0) return;
-        const uint32_t pair = info & 255, mi = info >> 8;
-        if (!warp_wait(b.v_raw(pair), (par >> pair) & 1, sh.abort_flag)) return;
+        const uint32_t pair = info;
+        if (!paged_warp_wait<T>(b.v_raw(pair), (par >> pair) & 1, sh.abort_flag)) return;
         par ^= 1u << pair;
-        const volatile uint32_t* mask =
-            reinterpret_cast<volatile uint32_t*>(sh.smem + T::kOffMask) + 4 * mi;
+        const volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(sh.tail_mask) + 4 * (i & 1);
         const uint32_t tile = sKV + (2 * pair + 1) * T::kTileBytes;
         for (int r = lane; r < 128; r += 32) {
             if ((mask[r >> 5] >> (r & 31)) & 1) continue;
@@ -745,7 +777,7 @@ __device__ void paged_mma(uint32_t tbase, const PagedBars<PagedTraits<D>>& b,
     uint32_t it = 0, units = 0;
     uint32_t q_used[2] = {0, 0}, o_used[2] = {0, 0}, p_par[2] = {0, 0};
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return mbar_wait(bar, parity, abort_flag, &g_attn_status);
+        return paged_wait<T>(bar, parity, abort_flag);
     };
     for (;; ++units) {
         const int ri = units % T::kUnits;
@@ -814,7 +846,7 @@ done: {
     // Every MMA issued so far must finish before tensor memory is released.
     volatile int no_abort = 0;
     mma_commit_w(b.drain(), 1);
-    mbar_wait(b.drain(), 0, &no_abort, &g_attn_status);
+    paged_wait<T>(b.drain(), 0, &no_abort);
 }
 }
 
@@ -864,7 +896,7 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
 
     for (uint32_t units = 0;; ++units) {
         const int ri = units % T::kUnits;
-        if (!warp_wait(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag)) return;
+        if (!paged_warp_wait<T>(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag)) return;
         const volatile PagedUnit& uu = ring[ri];
         const int kind = uu.kind, hk = uu.hk, tok0 = uu.tok, ntok = uu.ntok, pos0 = uu.pos0;
         const int len = uu.len, key0 = uu.key0, un[2] = {uu.n0, uu.n1}, slot = uu.slot;
@@ -884,7 +916,7 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
 
         for (int i = 0; i < n; ++i) {
             const int k = wide ? i : 2 * i + t;
-            if (!warp_wait(b.s_full(t), s_cnt & 1, abort_flag)) return;
+            if (!paged_warp_wait<T>(b.s_full(t), s_cnt & 1, abort_flag)) return;
             ++s_cnt;
             if (!active) {   // no row to work on: P stays what it is (rows are independent)
                 __syncwarp();
@@ -894,7 +926,7 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
             // the mask was written before K was loaded, and its entry is not written again
             // before this tile's P V has freed V's slot
             const uint32_t x = it + k;
-            if (!warp_wait(b.mask_full(x % T::kMasks), (x / T::kMasks) & 1, abort_flag)) return;
+            if (!paged_warp_wait<T>(b.mask_full(x % T::kMasks), (x / T::kMasks) & 1, abort_flag)) return;
             const uint4 mask = ld_shared_v4(masks + 16 * (x % T::kMasks));
             tc_fence_after_sync();
             uint32_t sr[128];
@@ -980,7 +1012,7 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
         // ---- epilogue
         const bool joins = !wide && un[1] > 0;   // group 0 joins both groups' results
         const bool used = n > 0;
-        if (used && !warp_wait(b.o_final(t), o_used[t] & 1, abort_flag)) return;
+        if (used && !paged_warp_wait<T>(b.o_final(t), o_used[t] & 1, abort_flag)) return;
         float w0 = 1.f, w1 = 0.f;
         if (joins) {
             if (t == 1) {
@@ -990,8 +1022,8 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
                 if (lane == 0) mbar_arrive(b.ml_full(0));
             } else {
                 // group 1 has waited for its own o_final by then
-                if (!warp_wait(b.ml_full(0), ml_cnt & 1, abort_flag)) return;
-                if (!warp_wait(b.o_final(1), o_used[1] & 1, abort_flag)) return;
+                if (!paged_warp_wait<T>(b.ml_full(0), ml_cnt & 1, abort_flag)) return;
+                if (!paged_warp_wait<T>(b.o_final(1), o_used[1] & 1, abort_flag)) return;
                 const float m1 = ml[r].x, l1 = ml[r].y;
                 const float m = fmaxf(m_ref, m1);
                 const float mb = m == -INFINITY ? 0.f : m;
@@ -1111,7 +1143,8 @@ __device__ __forceinline__ void paged_init(const PagedBars<T>& b, const PagedSha
     }
     for (int i = 0; i < T::kUnits; ++i) {
         mbar_init(b.unit_full(i), 1);
-        mbar_init(b.unit_empty(i), T::kIssuers + 9);   // the issuers, producer, 8 softmax warps
+        // read by the issuers, the producers and 8 softmax warps
+        mbar_init(b.unit_empty(i), T::kIssuers + T::kLoaders + 8);
     }
     for (int t = 0; t < 2; ++t) mbar_init(b.ml_full(t), 4);
     mbar_init(b.drain(), T::kIssuers);
@@ -1135,6 +1168,7 @@ __global__ void __launch_bounds__(PagedTraits<D>::kThreads, 1)
     sh.smem = smem;
     sh.abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     sh.tail_info = reinterpret_cast<int*>(tmem_holder + 2);
+    sh.tail_mask = tmem_holder + 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // the merge may be set up as soon as SMs have room; it waits for this grid's end
@@ -1163,7 +1197,7 @@ __global__ void __launch_bounds__(PagedTraits<D>::kThreads, 1)
     } else {
         regs_decrease<T::kOtherRegs>();
         if (warp == 8)
-            paged_producer<T, SPARSE>(p, &tm_q, &tm_k, &tm_v, b, sh, lane);
+            paged_producer<T, SPARSE, true, true>(p, &tm_q, &tm_k, &tm_v, b, sh, lane);
         else if (warp == 9) {
             if (lane == 0) paged_mma<D>(tbase, b, sh);
         } else if (warp == 10)
