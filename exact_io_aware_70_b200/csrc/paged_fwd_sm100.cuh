@@ -43,9 +43,6 @@
 namespace eattn {
 
 constexpr int kPagedMaxCtas = 160;     // slots of the workspace; the grid is at most this
-// Cost of starting a unit, and the least stretch worth a CTA of its own, in keys.
-constexpr int kPagedUnitCost = 128;
-constexpr int kPagedMinStretch = 512;
 constexpr int kPagedListMax = 480;     // entries of a sparse row's list of key runs
 
 // One CTA's partial rows of a unit that its stretch covers only in part.
@@ -71,6 +68,8 @@ struct PagedParams {
     int tpt, unit_tok;        // tokens of a Q tile and of a unit
     int page_shift, max_pages, num_pages;
     int causal;
+    // in keys: what starting a unit costs, and the least stretch worth a CTA of its own
+    int unit_cost, min_stretch;
     float scale_log2;
 };
 
@@ -214,6 +213,13 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
     return s;
 }
 
+// a / b for a >= 0, b > 0; the 64-bit division is long, and rarely needed
+__device__ __noinline__ long long div_long(long long a, long long b) { return a / b; }
+__device__ __forceinline__ long long div_fast(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return div_long(a, b);
+}
+
 // Lengths of a sequence's units on the line: unit q is base + min((q + 1) * U, n) *
 // slope long; begin(q) is where unit q starts within one head.
 struct PagedLine {
@@ -224,7 +230,7 @@ struct PagedLine {
         n = s.n;
         m = (s.n + U - 1) / U;
         slope = (!p.sel && p.causal) ? 1 : 0;
-        base = kPagedUnitCost +
+        base = p.unit_cost +
                (p.sel ? ((long long)p.K << p.page_shift) : p.causal ? max(s.len - s.n, 0) : s.len);
     }
     __device__ __forceinline__ long long unit(int q) const {
@@ -244,10 +250,11 @@ struct PagedLine {
 struct PagedStretch {
     long long offset, length;
     int b;
-    int block;   // sparse: tokens of a block of units (see paged_producer)
+    PagedSeq s;  // of sequence b
+    int block;   // sparse: tokens of a block of units (see PagedWalk)
 };
 
-// Run by the whole CTA. `red`: THREADS / 32 + 2 words of 64 bits.
+// Run by the whole CTA. `red`: THREADS / 32 + 4 words of 64 bits.
 template <int THREADS>
 __device__ __forceinline__ PagedStretch paged_schedule(const PagedParams& p, long long* red) {
     constexpr int kWarps = THREADS / 32;
@@ -272,19 +279,21 @@ __device__ __forceinline__ PagedStretch paged_schedule(const PagedParams& p, lon
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) total += red[w];
     __syncthreads();
-    long long chunk = (total + gridDim.x - 1) / gridDim.x;
-    if (chunk < kPagedMinStretch) chunk = kPagedMinStretch;
+    long long chunk = div_fast(total + gridDim.x - 1, gridDim.x);
+    if (chunk < p.min_stretch) chunk = p.min_stretch;
     PagedStretch st;
     st.block = 1;
     if (p.sel) {   // about as many tokens as one stretch holds for all K/V heads
         const long long all_heads =
-            (kPagedUnitCost + ((long long)p.K << p.page_shift)) * p.Hkv;
-        st.block = (int)min(max((chunk + all_heads / 2) / all_heads, 1ll), 1ll << 20);
+            (p.unit_cost + ((long long)p.K << p.page_shift)) * p.Hkv;
+        st.block = (int)min(max(div_fast(chunk + all_heads / 2, all_heads), 1ll), 1ll << 20);
     }
     const long long start = chunk * blockIdx.x;
     st.length = min(chunk, total - start);
     st.offset = 0;
     st.b = 0;
+    st.s.tok = st.s.n = st.s.len = 0;
+    st.s.bad = false;
     if (st.length <= 0) {   // the same for the whole CTA
         st.length = 0;
         return st;
@@ -309,14 +318,21 @@ __device__ __forceinline__ PagedStretch paged_schedule(const PagedParams& p, lon
         }
         incl += before;
         if (start >= incl - v && start < incl) {
+            const PagedSeq s = paged_seq(p, b);
             red[kWarps] = b;
             red[kWarps + 1] = start - (incl - v);
+            red[kWarps + 2] = s.tok;
+            red[kWarps + 3] = ((long long)s.n << 32) | s.len;
         }
         before += all;
         __syncthreads();
     }
     st.b = (int)red[kWarps];
     st.offset = red[kWarps + 1];
+    st.s.tok = (int)red[kWarps + 2];
+    st.s.n = (int)(red[kWarps + 3] >> 32);
+    st.s.len = (int)red[kWarps + 3];
+    st.s.bad = false;
     return st;
 }
 
@@ -354,19 +370,19 @@ struct PagedWalk {
     long long rem, left;     // where in unit q the stretch stands, and what is left of it
 
     __device__ __forceinline__ PagedWalk(const PagedParams& p, const PagedStretch& st)
-        : s(paged_seq(p, st.b)), line(p, s), sb(st.b), hk(0), q(0), q0(0), block(st.block),
+        : s(st.s), line(p, s), sb(st.b), hk(0), q(0), q0(0), block(st.block),
           rem(st.offset), left(st.length) {
         if (left <= 0) return;
         if constexpr (SPARSE) {
-            const long long i = rem / line.base;      // units before this one
+            const long long i = div_fast(rem, line.base);      // units before this one
             rem -= i * line.base;
-            q0 = (int)(i / ((long long)block * p.Hkv)) * block;
+            q0 = (int)div_fast(i, (long long)block * p.Hkv) * block;
             const int in = (int)(i - (long long)q0 * p.Hkv), nq = min(block, line.m - q0);
             hk = in / nq;
             q = q0 + in - hk * nq;
         } else {
             const long long head = line.begin(line.m);
-            hk = (int)(rem / head);
+            hk = (int)div_fast(rem, head);
             rem -= hk * head;
             // the last unit that begins at or before rem
             int hi = line.m - 1;
@@ -504,7 +520,7 @@ __device__ void paged_planner(const PagedParams& p, const PagedStretch& st, cons
             }
             const int all = max(tiles[0], tiles[1]);
             auto tile_at = [&](long long pos) -> int {
-                const long long k = (pos - kPagedUnitCost) >> 7;
+                const long long k = (pos - p.unit_cost) >> 7;
                 return k < 0 ? 0 : k > all ? all : (int)k;
             };
             const int k0 = p0 == 0 ? 0 : tile_at(p0);
@@ -803,7 +819,9 @@ __device__ void paged_mma(uint32_t tbase, const PagedBars<PagedTraits<D>>& b,
         auto issue_s = [&](int t, int i) -> bool {
             const int k = wide ? i : 2 * i + t;
             const uint32_t x = it + k, sk = 2 * (x % T::kPairs);
-            if (!wait(b.kv_full(sk), (x / T::kPairs) & 1)) return false;
+            // (tile 1 of a wide unit finds what tile 0 has waited for)
+            if (!(wide && t == 1 && i < n[0]) && !wait(b.kv_full(sk), (x / T::kPairs) & 1))
+                return false;
             tc_fence_after_sync();
             fwd_issue_s<D, false>(tbase + (t ? T::kColS1 : T::kColS0), dq[t], dk0 + sk * kTileStep, 1);
             mma_commit_w(b.s_full(t), 1);
@@ -815,7 +833,8 @@ __device__ void paged_mma(uint32_t tbase, const PagedBars<PagedTraits<D>>& b,
         auto issue_pv = [&](int t, int i) -> bool {
             const int k = wide ? i : 2 * i + t;
             const uint32_t x = it + k, sv = 2 * (x % T::kPairs) + 1;
-            if (!wait(b.kv_full(sv), (x / T::kPairs) & 1)) return false;
+            if (!(wide && t == 1 && i < n[0]) && !wait(b.kv_full(sv), (x / T::kPairs) & 1))
+                return false;
             if (!wait(b.p_full(t), p_par[t])) return false;
             p_par[t] ^= 1;
             if (i == 0 && o_used[t] > 0 && !wait(b.o_free(t), (o_used[t] - 1) & 1)) return false;
@@ -932,21 +951,14 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
             uint32_t sr[128];
             tmem_ld128(tS, sr);
             tmem_wait_ld128(sr);
-            if ((mask.x & mask.y & mask.z & mask.w) != 0xffffffffu) {
+            const int cl = (int)max(-1ll, min(128ll, (long long)lim - key0 - (long long)k * 128));
+            if (cl < 128 || (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu) {
+                // keys that exist and lie before the row's limit
+                const uint32_t seen[4] = {mask.x & low_bits(cl), mask.y & low_bits(cl - 32),
+                                          mask.z & low_bits(cl - 64), mask.w & low_bits(cl - 96)};
 #pragma unroll
-                for (int c = 0; c < 128; ++c) {
-                    const uint32_t word = c < 32 ? mask.x : c < 64 ? mask.y : c < 96 ? mask.z : mask.w;
-                    if (!((word >> (c & 31)) & 1)) sr[c] = __float_as_uint(-INFINITY);
-                }
-            }
-            {
-                const long long rest = (long long)lim - key0 - (long long)k * 128;
-                const int cl = (int)max(-1ll, min(128ll, rest));
-                if (cl < 128) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= cl) sr[c] = __float_as_uint(-INFINITY);
-                }
+                for (int c = 0; c < 128; ++c)
+                    if (!((seen[c >> 5] >> (c & 31)) & 1)) sr[c] = __float_as_uint(-INFINITY);
             }
             float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
@@ -987,7 +999,7 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
                 }
                 if (h == 0 && any_need && i > 0) {
                     // the commit that signalled S_t(i) covers P_t(i-1) V
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t orr[32];
                         tmem_ld32(tO + c, orr);
