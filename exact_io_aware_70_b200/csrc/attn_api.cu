@@ -686,6 +686,8 @@ int shift_of(int page_size) {
     return s;
 }
 
+int score_tiles(int max_pages) { return (max_pages + kScorePages - 1) / kScorePages; }
+
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // N = 0: 128-row tiles; else at most N rows per unit
@@ -941,41 +943,55 @@ attn_status_t attn_sparse_paged(const void* q, const void* k_cache, const void* 
 
 size_t attn_page_select_workspace_bytes(int T, int Hkv, int max_pages_per_seq) {
     if (T < 1 || Hkv < 1 || max_pages_per_seq < 1) return 0;
-    return round256((size_t)T * Hkv * max_pages_per_seq * 8);
+    const size_t rows = (size_t)T * Hkv;
+    return round256(rows * max_pages_per_seq * 8) + round256(rows * score_tiles(max_pages_per_seq) * 4);
 }
 
 }  // extern "C"
 
 namespace {
+template <int D, int THREADS, int PER>
+bool launch_topk(const SelectParams& p, cudaStream_t st) {
+    const long long rows = (long long)p.T * p.Hkv, groups = THREADS == 32 ? 4 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((rows + groups - 1) / groups));
+    cfg.blockDim = dim3(THREADS == 32 ? 128 : THREADS);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_page_topk_kernel<D, THREADS, PER>, p) == cudaSuccess;
+}
+
 template <int D>
 attn_status_t launch_select(const SelectParams& p, cudaStream_t st) {
-    const long long rows = (long long)p.T * p.Hkv;
-    const int smem = p.G * D * 8;
-    if (smem > 48 * 1024) {
-        const int dev = current_device();
-        if (dev < 0 || dev >= 64) return ATTN_ERR_CUDA;
+    constexpr int kSmem = (kScoreRows + kScorePages) * 4 * D;
+    const int dev = current_device();
+    if (dev < 0 || dev >= 64) return ATTN_ERR_CUDA;
+    {
         std::lock_guard<std::mutex> lk(g_dev_mu);
         bool& set = g_dev[dev].score_attr_set[D == 128 ? 1 : 0];
         if (!set) {
             if (cudaFuncSetAttribute(attn_page_score_kernel<D>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     128 * D * 8) != cudaSuccess)
+                                     kSmem) != cudaSuccess)
                 return ATTN_ERR_CUDA;
             set = true;
         }
     }
-    const dim3 grid((p.max_pages + kScoreThreads - 1) / kScoreThreads,
-                    (unsigned)(rows < 65535 ? rows : 65535), (unsigned)((rows + 65534) / 65535));
-    attn_page_score_kernel<D><<<grid, kScoreThreads, smem, st>>>(p);
-    // the least registers that hold a row's keys
-    if (p.max_pages <= 32 * 8)
-        attn_page_topk_kernel<32, 8><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p);
-    else if (p.max_pages <= 32 * 32)
-        attn_page_topk_kernel<32, 32><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p);
-    else if (p.max_pages <= 1024 * 4)
-        attn_page_topk_kernel<1024, 4><<<(unsigned)rows, 1024, 0, st>>>(p);
-    else
-        attn_page_topk_kernel<1024, 16><<<(unsigned)rows, 1024, 0, st>>>(p);
+    const dim3 grid((unsigned)((long long)p.tiles * ((p.T + p.tile_tok - 1) / p.tile_tok)), p.Hkv);
+    attn_page_score_kernel<D><<<grid, kScoreThreads, kSmem, st>>>(p);
+    // the fewest threads per row whose registers hold its keys
+    const bool ok = p.max_pages <= 32 * 8      ? launch_topk<D, 32, 8>(p, st)
+                    : p.max_pages <= 32 * 32   ? launch_topk<D, 32, 32>(p, st)
+                    : p.max_pages <= 256 * 16  ? launch_topk<D, 256, 16>(p, st)
+                                               : launch_topk<D, 1024, 16>(p, st);
+    if (!ok) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 }  // namespace
@@ -997,7 +1013,9 @@ attn_status_t attn_page_select(const void* q, const void* k_bounds, const int* b
         (long long)keep_first + keep_last > num_sel)
         return ATTN_ERR_INVALID_ARG;
     if (Hq / Hkv > 128 || max_pages_per_seq > 16384) return ATTN_ERR_UNSUPPORTED;
-    if ((long long)T * Hkv > (1ll << 30)) return ATTN_ERR_INVALID_ARG;
+    // rows and blocks are counted in 32 bits
+    if ((long long)T * Hkv > (1ll << 30) || (long long)T * score_tiles(max_pages_per_seq) > (1ll << 30))
+        return ATTN_ERR_INVALID_ARG;
     if (q_stride < (long long)Hq * d || q_stride > (1ll << 36)) return ATTN_ERR_INVALID_ARG;
     if (workspace_bytes < attn_page_select_workspace_bytes(T, Hkv, max_pages_per_seq))
         return ATTN_ERR_INVALID_ARG;
@@ -1013,6 +1031,12 @@ attn_status_t attn_page_select(const void* q, const void* k_bounds, const int* b
     p.seq_lens = seq_lens;
     p.sel = sel;
     p.keys = static_cast<unsigned long long*>(workspace);
+    p.err = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                     round256((size_t)T * Hkv * max_pages_per_seq * 8));
+    p.tiles = score_tiles(max_pages_per_seq);
+    // 64 rows at a time; where sequences have a token or two, a tile of one of them (its
+    // pages are its own)
+    p.tile_tok = (long long)T <= 2ll * B || Hq / Hkv > kScoreRows ? 1 : kScoreRows / (Hq / Hkv);
     p.q_stride = q_stride;
     p.B = B;
     p.T = T;

@@ -346,13 +346,19 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
 // ---------------------------------------------------------------- select --
 // Every query row t and K/V head hk gets the K pages whose keys can score
 // highest. For a page with bounds lo <= k <= hi (channel by channel),
-//   q . k <= sum_c (q_c >= 0 ? q_c hi_c : q_c lo_c),
+//   q . k <= sum_c (q_c >= 0 ? q_c hi_c : q_c lo_c) = [min(q, 0), max(q, 0)] . [lo, hi],
 // and a page's score is the largest such bound over the G query heads that
-// share hk. The products of two bf16 are exact in fp64 and their sum all but
-// is, so the choice does not depend on the order of the sum; pages with equal
-// scores are taken from the lowest up. Scores go to the workspace as 64-bit
-// keys of the same order; a second kernel finds each row's K-th largest key
-// bit by bit and writes the pages above it in ascending order.
+// share hk: a matrix product with 2 D terms, then a maximum. The choice has to be
+// that of exact scores (equal ones from the lowest page up), and 32-bit sums do
+// not tell near ones apart, so it is made in two steps:
+//   1. attn_page_score_kernel: the product on the tensor cores (bf16 products are
+//      exact, sums fp32), with a bound E of its error per row.
+//   2. attn_page_topk_kernel: a row's K-th largest score s, found bit by bit. A page
+//      above s + 2 E is chosen and one below s - 2 E is not, whatever the rounding;
+//      the few between are scored again in fp64 (where the sum of a row's exact products
+//      is all but exact) and the best of them fill up the choice.
+// Scoring every page in fp64 ran 287 us on 1053 rows x 8 heads x 246 pages (1.06e9
+// terms for 32 query heads); this SELECT_US us.
 struct SelectParams {
     const uint16_t* q;          // bf16 [T, Hq, D], q_stride elements from row to row
     const uint16_t* bounds;     // bf16 [num_pages, Hkv, 2, D]
@@ -360,10 +366,12 @@ struct SelectParams {
     const int* cu_q;            // [B + 1]
     const int* seq_lens;        // [B]
     int* sel;                   // [T, Hkv, K]
-    unsigned long long* keys;   // [T, Hkv, max_pages]
+    unsigned long long* keys;   // [T, Hkv, max_pages]: scores (fp32), then exact keys of a few
+    float* err;                 // [T, Hkv, score tiles]: error bounds
     long long q_stride;
     int B, T, Hq, Hkv, G, K, first, last;
-    int page_shift, max_pages, num_pages;
+    int page_shift, max_pages, num_pages, tiles;
+    int tile_tok;               // tokens of a score tile
 };
 
 struct SelectRow {
@@ -393,92 +401,226 @@ __device__ __forceinline__ SelectRow select_row(const SelectParams& p, int t) {
 }
 
 __device__ __forceinline__ unsigned long long order_key(double x) {
-    // ascending keys for ascending scores; NaN ranks above all scores, below the pages always kept
-    if (x != x) return ~1ull;
+    // ascending keys for ascending scores; NaN ranks above all scores
+    if (x != x) return ~0ull;
     const unsigned long long u = (unsigned long long)__double_as_longlong(x);
     return (u >> 63) ? ~u : (u | (1ull << 63));
 }
+// The same in 32 bits. Never 0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+    if (x != x) return ~0u;
+    const uint32_t u = __float_as_uint(x);
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
+}
 
-constexpr int kScoreThreads = 128;
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
-// Block (x, row): pages [x * kScoreThreads, + kScoreThreads) of a (t, hk), one
-// page per thread.
+// Block (x, hk): pages [64 (x % tiles), + 64) for the tile_tok tokens from (x / tiles) *
+// tile_tok on, one sequence of them after another. 64 rows (token, head of the group) at a time against 64
+// pages, 2 D terms: 64 KB of shared memory at D = 128, three blocks per SM; what bounds it is
+// the read of q and of the bounds (each tile of pages is read once per 64 rows), so the
+// products are left to mma.sync, which needs no set-up.
+constexpr int kScoreThreads = 128, kScorePages = 64, kScoreRows = 64;
+
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const SelectParams p) {
-    extern __shared__ double s_q[];   // [G][D]
-    const long long rowi = (long long)blockIdx.z * 65535 + blockIdx.y;
-    if (rowi >= (long long)p.T * p.Hkv) return;
-    const int t = (int)(rowi / p.Hkv), hk = (int)(rowi % p.Hkv);
-    const SelectRow row = select_row(p, t);
-    const int page0 = blockIdx.x * kScoreThreads;
-    if (page0 >= row.pages) return;
-    for (int i = threadIdx.x; i < p.G * D; i += kScoreThreads)
-        s_q[i] = (double)__uint_as_float(
-            (uint32_t)__ldg(p.q + (size_t)t * p.q_stride + (size_t)hk * p.G * D + i) << 16);
-    __syncthreads();
-    const int lp = page0 + threadIdx.x;
-    if (lp >= row.pages) return;
-    unsigned long long key = 0;       // a page that cannot be read is never chosen
-    const int page = __ldg(p.block_table + (size_t)row.b * p.max_pages + lp);
-    if (page < 0 || page >= p.num_pages) {
-        atomicOr(&g_attn_status, kDevErrBadIndex);
-    } else if (lp < p.first || lp >= row.pages - p.last) {
-        key = ~0ull;
-    } else {
-        const uint4* lo4 = reinterpret_cast<const uint4*>(p.bounds + ((size_t)page * p.Hkv + hk) * 2 * D);
-        const uint4* hi4 = lo4 + D / 8;
-        double best = -INFINITY;
-        bool nan = false;
-        for (int g0 = 0; g0 < p.G; g0 += 4) {
-            double acc[4] = {0, 0, 0, 0};
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 l = __ldg(lo4 + c), h = __ldg(hi4 + c);
-                const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, hw[4] = {h.x, h.y, h.z, h.w};
+    constexpr int kTerms = 2 * D, kRowBytes = 2 * kTerms, kChunks = kRowBytes / 16;
+    extern __shared__ __align__(128) uint8_t s_tiles[];
+    uint8_t* sA = s_tiles;                                // [64][2 D] bf16, 16-byte chunks swizzled
+    uint8_t* sB = s_tiles + kScoreRows * kRowBytes;       // [64 pages][2 D]
+    float* sS = reinterpret_cast<float*>(s_tiles);        // [64][65] scores, over A when it is done
+    __shared__ float s_sum[kScoreRows], s_red[kScoreThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int hk = blockIdx.y, tok_tile = blockIdx.x / p.tiles, tile = blockIdx.x - tok_tile * p.tiles;
+    const int page0 = tile * kScorePages;
+    const int t0 = tok_tile * p.tile_tok, t1 = min(t0 + p.tile_tok, p.T);
+    auto at = [](int row, int chunk) { return row * kRowBytes + ((chunk ^ (row & 7)) << 4); };
+
+    for (int t = t0; t < t1;) {
+        const SelectRow first = select_row(p, t);
+        if (first.b < 0) {
+            ++t;
+            continue;
+        }
+        // tokens [t, te) belong to this sequence; the last one sees most pages
+        const int te = min(t1, __ldg(p.cu_q + first.b + 1));
+        const int pages = select_row(p, te - 1).pages;
+        if (page0 >= pages) {
+            t = te;
+            continue;
+        }
+        __syncthreads();          // the last round's reads of shared memory are done
+        // ---- bounds of the tile's pages, and the largest of them
+        float top = 0.f;
+        constexpr int kRowsPerPass = kScoreThreads / kChunks, kBatch = 8;
+        const int c = tid % kChunks;
+        for (int r0 = tid / kChunks; r0 < kScorePages; r0 += kBatch * kRowsPerPass) {
+            uint4 x[kBatch];
+            int page[kBatch];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const double l0 = bf16_lo(lw[i]), l1 = bf16_hi(lw[i]);
-                    const double h0 = bf16_lo(hw[i]), h1 = bf16_hi(hw[i]);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const double* q = s_q + min(g0 + g, p.G - 1) * D + 8 * c + 2 * i;
-                        acc[g] = fma(q[0], q[0] >= 0 ? h0 : l0, acc[g]);
-                        acc[g] = fma(q[1], q[1] >= 0 ? h1 : l1, acc[g]);
-                    }
-                }
+            for (int k = 0; k < kBatch; ++k) {
+                const int lp = page0 + r0 + k * kRowsPerPass;
+                page[k] = r0 + k * kRowsPerPass < kScorePages && lp < pages
+                              ? __ldg(p.block_table + (size_t)first.b * p.max_pages + lp) : -1;
             }
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                nan = nan || acc[g] != acc[g];
-                best = fmax(best, acc[g]);
+            for (int k = 0; k < kBatch; ++k)
+                x[k] = page[k] >= 0 && page[k] < p.num_pages
+                           ? __ldg(reinterpret_cast<const uint4*>(
+                                       p.bounds + ((size_t)page[k] * p.Hkv + hk) * kTerms) + c)
+                           : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int row = r0 + k * kRowsPerPass;
+                if (row >= kScorePages) break;
+                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    top = fmax3(top, fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j])));
+                *reinterpret_cast<uint4*>(sB + at(row, c)) = x[k];
             }
         }
-        key = nan ? ~1ull : order_key(best);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        if (lane == 0) s_red[warp] = top;
+
+        // ---- rows, 64 at a time (more than one round only for groups of over 64 heads)
+        const int rows = (te - t) * p.G;
+        float best = -INFINITY;       // G > 64: of this thread's page, over the rounds
+        for (int r0 = 0; r0 < rows; r0 += kScoreRows) {
+            if (r0 > 0) __syncthreads();
+            if (tid < kScoreRows) s_sum[tid] = 0.f;
+            __syncthreads();
+            for (int i = tid; i < kScoreRows * (kChunks / 2); i += kScoreThreads) {
+                const int row = i / (kChunks / 2), c = i - row * (kChunks / 2);
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (r0 + row < rows) {
+                    const int tk = (r0 + row) / p.G, h = r0 + row - tk * p.G;
+                    x = __ldg(reinterpret_cast<const uint4*>(
+                                  p.q + (size_t)(t + tk) * p.q_stride + (size_t)(hk * p.G + h) * D) + c);
+                }
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t neg[4], pos[4];
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float a = bf16_lo(w[k]), b = bf16_hi(w[k]);
+                    sum += fabsf(a) + fabsf(b);
+                    // (a NaN goes with the negative part)
+                    const uint32_t keep = (a >= 0.f ? 0x0000FFFFu : 0u) | (b >= 0.f ? 0xFFFF0000u : 0u);
+                    pos[k] = w[k] & keep;
+                    neg[k] = w[k] & ~keep;
+                }
+                *reinterpret_cast<uint4*>(sA + at(row, c)) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+                *reinterpret_cast<uint4*>(sA + at(row, c + kChunks / 2)) =
+                    make_uint4(pos[0], pos[1], pos[2], pos[3]);
+                // the row's threads are neighbours in a warp
+#pragma unroll
+                for (int off = 1; off < kChunks / 2; off <<= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                if (c == 0) s_sum[row] = sum;
+            }
+            __syncthreads();
+            // ---- warp w: rows 16 w .. against all 64 pages
+            float acc[8][4];
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[n][k] = 0.f;
+            const uint32_t a0 = smem_addr(sA), b0 = smem_addr(sB);
+#pragma unroll 4
+            for (int kk = 0; kk < kTerms / 16; ++kk) {
+                uint32_t a[4];
+                ldmatrix_x4(a0 + at(16 * warp + (lane & 15), 2 * kk + (lane >> 4)), a);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {     // two groups of 8 pages each
+                    uint32_t b[4];
+                    ldmatrix_x4(b0 + at(16 * n + (lane & 7) + ((lane >> 4) << 3),
+                                        2 * kk + ((lane >> 3) & 1)), b);
+                    mma_16816(acc[2 * n], a, b[0], b[1]);
+                    mma_16816(acc[2 * n + 1], a, b[2], b[3]);
+                }
+            }
+            __syncthreads();                      // A is read
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const int row = 16 * warp + (lane >> 2), col = 8 * n + 2 * (lane & 3);
+                sS[row * 65 + col] = acc[n][0];
+                sS[row * 65 + col + 1] = acc[n][1];
+                sS[(row + 8) * 65 + col] = acc[n][2];
+                sS[(row + 8) * 65 + col + 1] = acc[n][3];
+            }
+            __syncthreads();
+            // ---- the largest over a token's heads
+            const int ntok = p.G <= kScoreRows ? te - t : 1;
+            const int heads = min(p.G, rows - r0 < kScoreRows ? rows - r0 : kScoreRows);
+            const int in = p.G <= kScoreRows ? p.G : heads;
+            for (int i = tid; i < ntok * kScorePages; i += kScoreThreads) {
+                const int tk = i / kScorePages, col = i - tk * kScorePages;
+                float m = best;
+                for (int h = 0; h < in; ++h) {
+                    const float x = sS[(tk * p.G + h) * 65 + col];
+                    m = (x > m || x != x) && m == m ? x : m;
+                }
+                if (p.G > kScoreRows && r0 + kScoreRows < rows) {
+                    best = m;
+                } else if (page0 + col < p.max_pages) {
+                    const size_t row = (size_t)(t + tk) * p.Hkv + hk;
+                    if (dcheck(t + tk < p.T))
+                        reinterpret_cast<float*>(p.keys + row * p.max_pages)[page0 + col] = m;
+                }
+            }
+            // ---- the error of these sums: 2 D / 16 steps that each add 17 numbers, every one of
+            // them cut off below 2^-23 of the largest at worst: under 2^-14 sum |q b|
+            if (tid < ntok) {
+                float sum = 0.f;
+                for (int h = 0; h < in; ++h) sum = fmaxf(sum, s_sum[tid * p.G + h]);
+                float b = s_red[0];
+                for (int w = 1; w < kScoreThreads / 32; ++w) b = fmaxf(b, s_red[w]);
+                float e = sum * b * 6.2e-5f;
+                float* dst = p.err + ((size_t)(t + tid) * p.Hkv + hk) * p.tiles + tile;
+                if (r0 > 0) e = fmaxf(e, *dst);   // this thread's own, of the first heads
+                if (dcheck(t + tid < p.T)) *dst = e;
+            }
+        }
+        t = te;
     }
-    p.keys[rowi * p.max_pages + lp] = key;
 }
 
 // One group of THREADS threads per (t, hk), PER keys in each thread's registers.
-template <int THREADS, int PER>
+template <int D, int THREADS, int PER>
 __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     attn_page_topk_kernel(const SelectParams p) {
     constexpr int kGroups = THREADS == 32 ? 4 : 1;       // rows per block
     constexpr int kWarps = THREADS / 32;
     __shared__ int s_cnt[2][kWarps];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the scores are made
     const int tid = threadIdx.x % THREADS, lane = tid & 31, warp = tid >> 5;
-    const long long rowi =
-        ((long long)blockIdx.y * gridDim.x + blockIdx.x) * kGroups + threadIdx.x / THREADS;
+    const long long rowi = (long long)blockIdx.x * kGroups + threadIdx.x / THREADS;
     if (rowi >= (long long)p.T * p.Hkv) return;
-    const int t = (int)(rowi / p.Hkv);
+    const int t = (int)(rowi / p.Hkv), hk = (int)(rowi - (long long)t * p.Hkv);
     const SelectRow row = select_row(p, t);
     if (row.b < 0) return;                               // rows of no sequence stay as they were
     int* out = p.sel + rowi * p.K;
-    // thread i holds pages r * THREADS + i
-    unsigned long long key[PER];
-#pragma unroll
-    for (int r = 0; r < PER; ++r) {
-        const int lp = r * THREADS + tid;
-        key[r] = lp < row.pages ? p.keys[rowi * p.max_pages + lp] : 0;
-    }
+    unsigned long long* exact = p.keys + rowi * p.max_pages;
+    const int* table = p.block_table + (size_t)row.b * p.max_pages;
     int flip = 0;
     auto total = [&](int v) -> int {
         v = __reduce_add_sync(0xffffffffu, v);
@@ -490,67 +632,168 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
         flip ^= 1;
         return v;
     };
-    // the K-th largest key (0: fewer than K pages can be read)
-    unsigned long long kth = 0;
-    int above = -1;
-    for (int bit = 63; bit >= 0; --bit) {
-        const unsigned long long cand = kth | (1ull << bit);
-        int n = 0;
-#pragma unroll
-        for (int r = 0; r < PER; ++r) n += key[r] >= cand;
-        n = total(n);
-        if (n >= p.K) kth = cand;
-        if (n == p.K) {                                   // exactly these: no need to go on
-            above = 0;
-            break;
+    // position of this thread among those with `x`, and how many there are
+    auto rank = [&](bool x, int& all) -> int {
+        const unsigned m = __ballot_sync(0xffffffffu, x);
+        int before = __popc(m & ((1u << lane) - 1));
+        all = __popc(m);
+        if (kWarps > 1) {
+            if (lane == 0) s_cnt[flip][warp] = all;
+            __syncthreads();
+            all = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) before += s_cnt[flip][w];
+                all += s_cnt[flip][w];
+            }
+            flip ^= 1;
         }
-    }
-    if (kth == 0) kth = 1;                               // key 0 marks what cannot be chosen
-    // how many of the keys equal to the K-th are taken, from the lowest page up
-    int gt = 0;
-    if (above != 0) {
-#pragma unroll
-        for (int r = 0; r < PER; ++r) gt += key[r] > kth;
-        gt = total(gt);
-    }
-    int ties = above == 0 ? 0x7fffffff : p.K - gt;
-    int at = 0;                                          // pages written so far
+        return before;
+    };
+    // thread i holds pages r * THREADS + i; key 0: not to be ranked
+    uint32_t key[PER];
+    uint32_t keep = 0;                                   // bit r: always chosen
+    int kept = 0, ranked = 0;
+    bool bad = false;
 #pragma unroll
     for (int r = 0; r < PER; ++r) {
-        if (r * THREADS >= row.pages) break;             // the same for the whole group
-        const bool eq = above != 0 && key[r] == kth;
-        bool take = above == 0 ? key[r] >= kth : key[r] > kth;
-        // position among this round's equal keys, then among its chosen ones
-        const unsigned lt = (1u << lane) - 1;
-        unsigned me = __ballot_sync(0xffffffffu, eq);
-        int eq_before = 0, eq_all = __popc(me);
-        if (kWarps > 1) {
-            if (lane == 0) s_cnt[flip][warp] = eq_all;
-            __syncthreads();
-            eq_all = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) eq_before += s_cnt[flip][w];
-                eq_all += s_cnt[flip][w];
+        const int lp = r * THREADS + tid;
+        key[r] = 0;
+        if (lp < row.pages) {
+            const int page = __ldg(table + lp);
+            if (page < 0 || page >= p.num_pages) {
+                bad = true;
+            } else if (lp < p.first || lp >= row.pages - p.last) {
+                keep |= 1u << r;
+                ++kept;
+            } else {
+                key[r] = order_key(reinterpret_cast<const float*>(exact)[lp]);
+                ++ranked;
             }
-            flip ^= 1;
         }
-        if (eq && eq_before + __popc(me & lt) < ties) take = true;
-        ties = max(0, ties - eq_all);
-        const unsigned mt = __ballot_sync(0xffffffffu, take);
-        int tk_before = 0, tk_all = __popc(mt);
-        if (kWarps > 1) {
-            if (lane == 0) s_cnt[flip][warp] = tk_all;
-            __syncthreads();
-            tk_all = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) tk_before += s_cnt[flip][w];
-                tk_all += s_cnt[flip][w];
+    }
+    if (bad) atomicOr(&g_attn_status, kDevErrBadIndex);
+    const int want = p.K - total(kept);                  // to be chosen by their scores
+    ranked = total(ranked);
+    float err = 0.f;
+    for (int i = 0; i * kScorePages < row.pages; ++i)
+        err = fmaxf(err, p.err[rowi * p.tiles + i]);
+
+    // bit r: chosen for certain / to be ranked by exact keys
+    uint32_t sure = keep, maybe = 0;
+    int need = 0, unsure = 0;
+    if (ranked <= want) {
+#pragma unroll
+        for (int r = 0; r < PER; ++r) sure |= (key[r] != 0) << r;
+    } else if (want > 0) {
+        uint32_t kth = 0;                                // the want-th largest key
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t cand = kth | (1u << bit);
+            int n = 0;
+#pragma unroll
+            for (int r = 0; r < PER; ++r) n += key[r] >= cand;
+            if (total(n) >= want) kth = cand;
+        }
+        const float s = key_value(kth);
+        const float above = s + 2.0f * err, below = s - 2.0f * err;
+        int n = 0, m = 0;
+#pragma unroll
+        for (int r = 0; r < PER; ++r) {
+            const float v = key_value(key[r]);
+            // (comparisons with NaN are false: undecided)
+            const bool yes = key[r] != 0 && v > above, no = key[r] == 0 || v < below;
+            sure |= (uint32_t)yes << r;
+            maybe |= (uint32_t)(!yes && !no) << r;
+            n += yes;
+            m += !yes && !no;
+        }
+        need = want - total(n);
+        unsure = total(m);
+        if (unsure <= need) {
+            sure |= maybe;
+            maybe = 0;
+        }
+    }
+    // ---- exact keys of the undecided pages, in page order
+    unsigned long long kth = 0;
+    int ties = 0;
+    if (unsure > need) {
+        __syncwarp();
+        if (kWarps > 1) __syncthreads();                 // all scores are in registers
+        int base = 0;
+#pragma unroll 1
+        for (int r = 0; r * THREADS < row.pages; ++r) {
+            int all;
+            const int before = rank((maybe >> r) & 1, all);
+            if (all == 0) continue;
+            unsigned m = __ballot_sync(0xffffffffu, (maybe >> r) & 1);
+            while (m && err == 0.f) {                    // no rounding at all: they are equal
+                const int src = __ffs(m) - 1;
+                m &= m - 1;
+                const int place = base + __shfl_sync(0xffffffffu, before, src);
+                if (lane == 0 && dcheck(place < p.max_pages)) exact[place] = 1;
             }
-            flip ^= 1;
+            while (m) {                                  // a warp scores its own pages
+                const int src = __ffs(m) - 1;
+                m &= m - 1;
+                const int lp = r * THREADS + warp * 32 + src;
+                const uint16_t* bnd = p.bounds + ((size_t)__ldg(table + lp) * p.Hkv + hk) * 2 * D;
+                double best = -INFINITY;
+                bool nan = false;
+                for (int g = 0; g < p.G; ++g) {
+                    const uint16_t* q = p.q + (size_t)t * p.q_stride + (size_t)(hk * p.G + g) * D;
+                    double sum = 0;
+#pragma unroll
+                    for (int c = lane; c < D; c += 32) {
+                        const float x = __uint_as_float((uint32_t)__ldg(q + c) << 16);
+                        const float lo = __uint_as_float((uint32_t)__ldg(bnd + c) << 16);
+                        const float hi = __uint_as_float((uint32_t)__ldg(bnd + D + c) << 16);
+                        sum = fma((double)x, (double)(x >= 0.f ? hi : lo), sum);
+                    }
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1)
+                        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                    nan = nan || sum != sum;
+                    best = fmax(best, sum);
+                }
+                const int place = base + __shfl_sync(0xffffffffu, before, src);
+                if (lane == 0 && dcheck(place < p.max_pages))
+                    exact[place] = nan ? ~0ull : order_key(best);
+            }
+            base += all;
         }
-        const int pos = at + tk_before + __popc(mt & lt);
+        __syncwarp();
+        if (kWarps > 1) __syncthreads();
+        // the need-th largest of them
+        for (int bit = 63; bit >= 0; --bit) {
+            const unsigned long long cand = kth | (1ull << bit);
+            int n = 0;
+            for (int i = tid; i < unsure; i += THREADS) n += exact[i] >= cand;
+            if (total(n) >= need) kth = cand;
+        }
+        int n = 0;
+        for (int i = tid; i < unsure; i += THREADS) n += exact[i] > kth;
+        ties = need - total(n);                          // of the equal ones, from the lowest page up
+    }
+    // ---- the chosen pages in ascending order
+    int at = 0, base = 0;
+#pragma unroll 1
+    for (int r = 0; r * THREADS < row.pages; ++r) {
+        bool take = (sure >> r) & 1;
+        if (unsure > need) {
+            const bool open = (maybe >> r) & 1;
+            int all;
+            const int place = base + rank(open, all);
+            const unsigned long long k = open ? exact[place] : 0;
+            int equal;
+            const int eq = rank(open && k == kth, equal);
+            take = take || (open && (k > kth || (k == kth && eq < ties)));
+            ties = max(0, ties - equal);
+            base += all;
+        }
+        int all;
+        const int pos = at + rank(take, all);
         if (take && dcheck(pos < p.K)) out[pos] = r * THREADS + tid;
-        at += tk_all;
+        at += all;
     }
     for (int i = at + tid; i < p.K; i += THREADS) out[i] = -1;
 }

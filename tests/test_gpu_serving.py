@@ -335,6 +335,9 @@ def test_fwd_long_offsets():
     ([2], [5000], 28, 4, 128, 16, 40, 2, 3),
     ([1], [20000], 4, 1, 64, 16, 100, 0, 1),
     ([3], [300], 40, 1, 64, 32, 20, 1, 1),
+    ([3, 20], [1500, 40], 100, 1, 128, 16, 20, 1, 0),
+    ([1], [70000], 2, 2, 64, 16, 50, 1, 1),
+    ([17, 1, 9], [1100, 1023, 2000], 16, 2, 128, 16, 30, 0, 1),
 ])
 def test_select_matches_definition(new, ctx, Hq, Hkv, d, ps, K, first, last):
     m = gpu_util.ea()
@@ -365,6 +368,29 @@ def test_select_many_equal_scores_and_bad_pages():
                        0, 1, ws)
     assert m.attn_status() == m.ATTN_ERR_BAD_INDEX
     assert torch.equal(sel.cpu(), pu.ref_select(s, kb, 9, 0, 1))
+
+
+@pytest.mark.parametrize("ps,ctx", [(16, 1500), (16, 30000)])
+def test_select_near_scores(ps, ctx):
+    """Pages whose scores differ by less than 32-bit sums can tell, and rows of zeros."""
+    m = gpu_util.ea()
+    s = pu.make_step([2, 1], [ctx, 40], 4, 1, 128, ps, seed=5, poison=False)
+    s.q[2] = 0
+    kb = pu.page_bounds(s.kc)
+    base = kb[s.table[0, 0].long()].clone()
+    for i in range(ctx // ps):
+        row = base.clone()
+        row[0, 1] = base[0, 1] * 2.0 ** -(i % 5)          # the largest key of one channel shrinks,
+        row[0, 1, 2:] = base[0, 1, 2:]                      # in the first two channels alone
+        row[0, 1, 0] = 2.0 ** -20 * (1 + (i * 7919) % 97)   # and by next to nothing in one
+        kb[s.table[0, i].long()] = row
+    sel = torch.full((3, 1, 9), -7, dtype=torch.int32, device="cuda")
+    ws = torch.empty(m.attn_page_select_workspace_bytes(3, 1, s.max_pages), dtype=torch.uint8,
+                     device="cuda")
+    m.attn_page_select(s.q.cuda(), kb.cuda(), s.table.cuda(), s.cu.cuda(), s.seq.cuda(), sel, ps,
+                       1, 1, ws)
+    assert m.attn_status() == 0
+    assert torch.equal(sel.cpu(), pu.ref_select(s, kb, 9, 1, 1))
 
 
 @pytest.mark.parametrize("new,ctx,Hq,Hkv,d,ps,K", [
