@@ -131,7 +131,7 @@ struct DeviceInfo {
     int sms = 0;
     bool paged_attr_set[12] = {};
     bool tables_attr_set = false;
-    bool score_attr_set[2] = {false, false};
+    bool score_attr_set[4] = {};
     bool fwd_attr_set[8] = {false, false, false, false, false, false, false, false};
     bool bwd_attr_set[4] = {false, false, false, false};
 };
@@ -965,27 +965,37 @@ bool launch_topk(const SelectParams& p, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, attn_page_topk_kernel<D, THREADS, PER>, p) == cudaSuccess;
 }
 
-template <int D>
-attn_status_t launch_select(const SelectParams& p, cudaStream_t st) {
-    constexpr int kSmem = (kScoreRows + kScorePages) * 4 * D;
+template <int D, int ROWS>
+bool launch_score(const SelectParams& p, cudaStream_t st) {
+    constexpr int kSmem = (ROWS + kScorePages) * 4 * D;
     const int dev = current_device();
-    if (dev < 0 || dev >= 64) return ATTN_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return false;
     {
         std::lock_guard<std::mutex> lk(g_dev_mu);
-        bool& set = g_dev[dev].score_attr_set[D == 128 ? 1 : 0];
+        bool& set = g_dev[dev].score_attr_set[(D == 128 ? 1 : 0) + (ROWS == 64 ? 2 : 0)];
         if (!set) {
-            if (cudaFuncSetAttribute(attn_page_score_kernel<D>,
+            if (cudaFuncSetAttribute(attn_page_score_kernel<D, ROWS>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kSmem) != cudaSuccess)
-                return ATTN_ERR_CUDA;
+                return false;
             set = true;
         }
     }
     const dim3 grid((unsigned)((long long)p.tiles * ((p.T + p.tile_tok - 1) / p.tile_tok)), p.Hkv);
-    attn_page_score_kernel<D><<<grid, kScoreThreads, kSmem, st>>>(p);
+    attn_page_score_kernel<D, ROWS><<<grid, kScoreThreads, kSmem, st>>>(p);
+    return true;
+}
+
+template <int D>
+attn_status_t launch_select(const SelectParams& p, cudaStream_t st) {
+    if (!(p.tile_tok * p.G <= 16 ? launch_score<D, 16>(p, st) : launch_score<D, 64>(p, st)))
+        return ATTN_ERR_CUDA;
     // the fewest threads per row whose registers hold its keys
     const bool ok = p.max_pages <= 32 * 8      ? launch_topk<D, 32, 8>(p, st)
-                    : p.max_pages <= 32 * 32   ? launch_topk<D, 32, 32>(p, st)
+                    // few rows: more threads for each, or the row's own steps set the time
+                    : p.max_pages <= 32 * 32   ? ((long long)p.T * p.Hkv <= 1024
+                                                      ? launch_topk<D, 128, 8>(p, st)
+                                                      : launch_topk<D, 32, 32>(p, st))
                     : p.max_pages <= 256 * 16  ? launch_topk<D, 256, 16>(p, st)
                                                : launch_topk<D, 1024, 16>(p, st);
     if (!ok) {
@@ -1034,9 +1044,9 @@ attn_status_t attn_page_select(const void* q, const void* k_bounds, const int* b
     p.err = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                      round256((size_t)T * Hkv * max_pages_per_seq * 8));
     p.tiles = score_tiles(max_pages_per_seq);
-    // 64 rows at a time; where sequences have a token or two, a tile of one of them (its
+    // 64 tokens share a tile's read of the bounds; where sequences have a token or two, one (its
     // pages are its own)
-    p.tile_tok = (long long)T <= 2ll * B || Hq / Hkv > kScoreRows ? 1 : kScoreRows / (Hq / Hkv);
+    p.tile_tok = (long long)T <= 2ll * B ? 1 : 64;
     p.q_stride = q_stride;
     p.B = B;
     p.T = T;

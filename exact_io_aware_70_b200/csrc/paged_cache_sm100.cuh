@@ -375,28 +375,31 @@ struct SelectParams {
 };
 
 struct SelectRow {
-    int b, pages;    // sequence (-1: none), visible pages
+    int b, end;       // sequence (-1: none), the row after its last one
+    int pos, pages;   // the row's position, and the pages it sees
 };
 
-// The sequence of row t and how many pages the row sees.
-__device__ __forceinline__ SelectRow select_row(const SelectParams& p, int t) {
+// The sequence of row t, where its rows end and how many pages the row sees; by a whole warp.
+__device__ __forceinline__ SelectRow select_row(const SelectParams& p, int t, int lane) {
     SelectRow r;
     r.b = -1;
-    r.pages = 0;
-    if (t < __ldg(p.cu_q) || t >= __ldg(p.cu_q + p.B)) return r;
-    int lo = 0, hi = p.B;    // the last b with cu[b] <= t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(p.cu_q + mid) <= t) lo = mid;
-        else hi = mid;
+    r.pages = r.end = 0;
+    // the last b with cu[b] <= t, 32 places at a time
+    int lo = 0, n = p.B;          // it is in [lo, lo + n), or t lies before the first row
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const bool le = lane * step < n && (lane == 0 || __ldg(p.cu_q + at) <= t);
+        const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;   // (offsets ascend)
+        lo += k * step;
+        n = min(step, n - k * step);
     }
-    const int c0 = __ldg(p.cu_q + lo), c1 = __ldg(p.cu_q + lo + 1);
-    if (t < c0 || t >= c1) return r;   // offsets that do not ascend
-    const int cap = p.max_pages << p.page_shift;
-    const int l = __ldg(p.seq_lens + lo), len = min(max(l, 0), cap);
+    const int c0 = __ldg(p.cu_q + lo), c1 = __ldg(p.cu_q + lo + 1), l = __ldg(p.seq_lens + lo);
+    if (t < c0 || t >= c1) return r;   // before the first, past the last, or offsets that do not ascend
+    const int len = min(max(l, 0), p.max_pages << p.page_shift);
     r.b = lo;
-    const long long pos = (long long)len - c1 + t;
-    r.pages = pos < 0 ? 0 : (int)(pos >> p.page_shift) + 1;
+    r.end = c1;
+    r.pos = len - c1 + t;
+    r.pages = r.pos < 0 ? 0 : (r.pos >> p.page_shift) + 1;
     return r;
 }
 
@@ -432,41 +435,42 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 }
 
 // Block (x, hk): pages [64 (x % tiles), + 64) for the tile_tok tokens from (x / tiles) *
-// tile_tok on, one sequence of them after another. 64 rows (token, head of the group) at a time against 64
-// pages, 2 D terms: 64 KB of shared memory at D = 128, three blocks per SM; what bounds it is
-// the read of q and of the bounds (each tile of pages is read once per 64 rows), so the
-// products are left to mma.sync, which needs no set-up.
-constexpr int kScoreThreads = 128, kScorePages = 64, kScoreRows = 64;
+// tile_tok on, one sequence of them after another. ROWS = 64 or 16 rows (token, head of the
+// group) at a time against 64 pages, 2 D terms: 64 or 40 KB of shared memory at D = 128. What
+// bounds it is the read of q and of the bounds (each tile of pages is read once per ROWS
+// rows), so the products are left to mma.sync, which needs no set-up.
+constexpr int kScoreThreads = 128, kScorePages = 64;
 
-template <int D>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const SelectParams p) {
     constexpr int kTerms = 2 * D, kRowBytes = 2 * kTerms, kChunks = kRowBytes / 16;
     extern __shared__ __align__(128) uint8_t s_tiles[];
-    uint8_t* sA = s_tiles;                                // [64][2 D] bf16, 16-byte chunks swizzled
-    uint8_t* sB = s_tiles + kScoreRows * kRowBytes;       // [64 pages][2 D]
-    float* sS = reinterpret_cast<float*>(s_tiles);        // [64][65] scores, over A when it is done
-    __shared__ float s_sum[kScoreRows], s_red[kScoreThreads / 32];
+    uint8_t* sA = s_tiles;                                // [ROWS][2 D] bf16, 16-byte chunks swizzled
+    uint8_t* sB = s_tiles + ROWS * kRowBytes;             // [64 pages][2 D]
+    float* sS = reinterpret_cast<float*>(s_tiles);        // [ROWS][65] scores, over A when it is done
+    __shared__ float s_sum[ROWS], s_red[kScoreThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hk = blockIdx.y, tok_tile = blockIdx.x / p.tiles, tile = blockIdx.x - tok_tile * p.tiles;
     const int page0 = tile * kScorePages;
     const int t0 = tok_tile * p.tile_tok, t1 = min(t0 + p.tile_tok, p.T);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the choice waits by itself
     auto at = [](int row, int chunk) { return row * kRowBytes + ((chunk ^ (row & 7)) << 4); };
 
     for (int t = t0; t < t1;) {
-        const SelectRow first = select_row(p, t);
+        const SelectRow first = select_row(p, t, lane);
         if (first.b < 0) {
             ++t;
             continue;
         }
         // tokens [t, te) belong to this sequence; the last one sees most pages
-        const int te = min(t1, __ldg(p.cu_q + first.b + 1));
-        const int pages = select_row(p, te - 1).pages;
+        const int te = min(t1, first.end), last_pos = first.pos + te - 1 - t;
+        const int pages = last_pos < 0 ? 0 : (last_pos >> p.page_shift) + 1;
         if (page0 >= pages) {
             t = te;
             continue;
         }
         __syncthreads();          // the last round's reads of shared memory are done
-        // ---- bounds of the tile's pages, and the largest of them
+        // ---- bounds of the tile's pages, and the largest sum of squares of one page's
         float top = 0.f;
         constexpr int kRowsPerPass = kScoreThreads / kChunks, kBatch = 8;
         const int c = tid % kChunks;
@@ -487,12 +491,18 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
                            : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const int row = r0 + k * kRowsPerPass;
-                if (row >= kScorePages) break;
+                const int row = r0 + k * kRowsPerPass;   // (kScorePages is a multiple of a batch)
                 const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    top = fmax3(top, fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j])));
+                for (int j = 0; j < 4; ++j) {
+                    sum = fmaf(bf16_lo(w[j]), bf16_lo(w[j]), sum);
+                    sum = fmaf(bf16_hi(w[j]), bf16_hi(w[j]), sum);
+                }
+#pragma unroll
+                for (int off = 1; off < kChunks; off <<= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                top = fmaxf(top, sum);
                 *reinterpret_cast<uint4*>(sB + at(row, c)) = x[k];
             }
         }
@@ -501,20 +511,22 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
         if (lane == 0) s_red[warp] = top;
 
-        // ---- rows, 64 at a time (more than one round only for groups of over 64 heads)
-        const int rows = (te - t) * p.G;
-        float best = -INFINITY;       // G > 64: of this thread's page, over the rounds
-        for (int r0 = 0; r0 < rows; r0 += kScoreRows) {
-            if (r0 > 0) __syncthreads();
-            if (tid < kScoreRows) s_sum[tid] = 0.f;
+        // ---- its rows, as many tokens at a time as fit ROWS (G > ROWS: one, in rounds)
+        const int sub = max(1, ROWS / p.G);
+        for (int s0 = t; s0 < te; s0 += sub) {
+        const int rows = (min(te, s0 + sub) - s0) * p.G;
+        float best = -INFINITY;       // G > ROWS: of this thread's page, over the rounds
+        for (int r0 = 0; r0 < rows; r0 += ROWS) {
+            __syncthreads();          // (the last reads of A, scores and sums)
+            if (tid < ROWS) s_sum[tid] = 0.f;
             __syncthreads();
-            for (int i = tid; i < kScoreRows * (kChunks / 2); i += kScoreThreads) {
+            for (int i = tid; i < ROWS * (kChunks / 2); i += kScoreThreads) {
                 const int row = i / (kChunks / 2), c = i - row * (kChunks / 2);
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (r0 + row < rows) {
                     const int tk = (r0 + row) / p.G, h = r0 + row - tk * p.G;
                     x = __ldg(reinterpret_cast<const uint4*>(
-                                  p.q + (size_t)(t + tk) * p.q_stride + (size_t)(hk * p.G + h) * D) + c);
+                                  p.q + (size_t)(s0 + tk) * p.q_stride + (size_t)(hk * p.G + h) * D) + c);
                 }
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                 uint32_t neg[4], pos[4];
@@ -522,7 +534,7 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float a = bf16_lo(w[k]), b = bf16_hi(w[k]);
-                    sum += fabsf(a) + fabsf(b);
+                    sum = fmaf(a, a, fmaf(b, b, sum));
                     // (a NaN goes with the negative part)
                     const uint32_t keep = (a >= 0.f ? 0x0000FFFFu : 0u) | (b >= 0.f ? 0xFFFF0000u : 0u);
                     pos[k] = w[k] & keep;
@@ -538,21 +550,23 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
                 if (c == 0) s_sum[row] = sum;
             }
             __syncthreads();
-            // ---- warp w: rows 16 w .. against all 64 pages
-            float acc[8][4];
+            // ---- warp w: rows 16 w .. against all 64 pages, or 16 rows against pages 16 w ..
+            constexpr int kN = ROWS / 16;             // groups of 16 pages per warp
+            const int wr = ROWS == 64 ? 16 * warp : 0, wp = ROWS == 64 ? 0 : 16 * warp;
+            float acc[2 * kN][4];
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
+            for (int n = 0; n < 2 * kN; ++n)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[n][k] = 0.f;
             const uint32_t a0 = smem_addr(sA), b0 = smem_addr(sB);
 #pragma unroll 4
             for (int kk = 0; kk < kTerms / 16; ++kk) {
                 uint32_t a[4];
-                ldmatrix_x4(a0 + at(16 * warp + (lane & 15), 2 * kk + (lane >> 4)), a);
+                ldmatrix_x4(a0 + at(wr + (lane & 15), 2 * kk + (lane >> 4)), a);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {     // two groups of 8 pages each
+                for (int n = 0; n < kN; ++n) {    // two groups of 8 pages each
                     uint32_t b[4];
-                    ldmatrix_x4(b0 + at(16 * n + (lane & 7) + ((lane >> 4) << 3),
+                    ldmatrix_x4(b0 + at(wp + 16 * n + (lane & 7) + ((lane >> 4) << 3),
                                         2 * kk + ((lane >> 3) & 1)), b);
                     mma_16816(acc[2 * n], a, b[0], b[1]);
                     mma_16816(acc[2 * n + 1], a, b[2], b[3]);
@@ -560,8 +574,8 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
             }
             __syncthreads();                      // A is read
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                const int row = 16 * warp + (lane >> 2), col = 8 * n + 2 * (lane & 3);
+            for (int n = 0; n < 2 * kN; ++n) {
+                const int row = wr + (lane >> 2), col = wp + 8 * n + 2 * (lane & 3);
                 sS[row * 65 + col] = acc[n][0];
                 sS[row * 65 + col + 1] = acc[n][1];
                 sS[(row + 8) * 65 + col] = acc[n][2];
@@ -569,9 +583,9 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
             }
             __syncthreads();
             // ---- the largest over a token's heads
-            const int ntok = p.G <= kScoreRows ? te - t : 1;
-            const int heads = min(p.G, rows - r0 < kScoreRows ? rows - r0 : kScoreRows);
-            const int in = p.G <= kScoreRows ? p.G : heads;
+            const int ntok = p.G <= ROWS ? rows / p.G : 1;
+            const int heads = min(p.G, rows - r0 < ROWS ? rows - r0 : ROWS);
+            const int in = p.G <= ROWS ? p.G : heads;
             for (int i = tid; i < ntok * kScorePages; i += kScoreThreads) {
                 const int tk = i / kScorePages, col = i - tk * kScorePages;
                 float m = best;
@@ -579,26 +593,28 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
                     const float x = sS[(tk * p.G + h) * 65 + col];
                     m = (x > m || x != x) && m == m ? x : m;
                 }
-                if (p.G > kScoreRows && r0 + kScoreRows < rows) {
+                if (p.G > ROWS && r0 + ROWS < rows) {
                     best = m;
                 } else if (page0 + col < p.max_pages) {
-                    const size_t row = (size_t)(t + tk) * p.Hkv + hk;
-                    if (dcheck(t + tk < p.T))
+                    const size_t row = (size_t)(s0 + tk) * p.Hkv + hk;
+                    if (dcheck(s0 + tk < p.T))
                         reinterpret_cast<float*>(p.keys + row * p.max_pages)[page0 + col] = m;
                 }
             }
-            // ---- the error of these sums: 2 D / 16 steps that each add 17 numbers, every one of
-            // them cut off below 2^-23 of the largest at worst: under 2^-14 sum |q b|
+            // ---- the error of these sums: 2 D / 16 <= 16 steps that each add 17 numbers, every one
+            // of them cut off below 2^-23 of the largest at worst: under 16 * 17 * 2^-23 < 3.3e-5
+            // times sum |q b| <= |q| |b|
             if (tid < ntok) {
                 float sum = 0.f;
                 for (int h = 0; h < in; ++h) sum = fmaxf(sum, s_sum[tid * p.G + h]);
                 float b = s_red[0];
                 for (int w = 1; w < kScoreThreads / 32; ++w) b = fmaxf(b, s_red[w]);
-                float e = sum * b * 6.2e-5f;
-                float* dst = p.err + ((size_t)(t + tid) * p.Hkv + hk) * p.tiles + tile;
+                float e = sqrtf(sum) * sqrtf(b) * 3.3e-5f;
+                float* dst = p.err + ((size_t)(s0 + tid) * p.Hkv + hk) * p.tiles + tile;
                 if (r0 > 0) e = fmaxf(e, *dst);   // this thread's own, of the first heads
-                if (dcheck(t + tid < p.T)) *dst = e;
+                if (dcheck(s0 + tid < p.T)) *dst = e;
             }
+        }
         }
         t = te;
     }
@@ -616,7 +632,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     const long long rowi = (long long)blockIdx.x * kGroups + threadIdx.x / THREADS;
     if (rowi >= (long long)p.T * p.Hkv) return;
     const int t = (int)(rowi / p.Hkv), hk = (int)(rowi - (long long)t * p.Hkv);
-    const SelectRow row = select_row(p, t);
+    const SelectRow row = select_row(p, t, lane);
     if (row.b < 0) return;                               // rows of no sequence stay as they were
     int* out = p.sel + rowi * p.K;
     unsigned long long* exact = p.keys + rowi * p.max_pages;
@@ -629,6 +645,15 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
         __syncthreads();
         v = 0;
         for (int w = 0; w < kWarps; ++w) v += s_cnt[flip][w];
+        flip ^= 1;
+        return v;
+    };
+    auto lowest = [&](uint32_t v) -> uint32_t {
+        v = __reduce_min_sync(0xffffffffu, v);
+        if (kWarps == 1) return v;
+        if (lane == 0) s_cnt[flip][warp] = (int)v;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) v = min(v, (uint32_t)s_cnt[flip][w]);
         flip ^= 1;
         return v;
     };
@@ -675,8 +700,9 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     const int want = p.K - total(kept);                  // to be chosen by their scores
     ranked = total(ranked);
     float err = 0.f;
-    for (int i = 0; i * kScorePages < row.pages; ++i)
-        err = fmaxf(err, p.err[rowi * p.tiles + i]);
+    for (int i = lane; i * kScorePages < row.pages; i += 32) err = fmaxf(err, p.err[rowi * p.tiles + i]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, off));
 
     // bit r: chosen for certain / to be ranked by exact keys
     uint32_t sure = keep, maybe = 0;
@@ -685,13 +711,32 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
 #pragma unroll
         for (int r = 0; r < PER; ++r) sure |= (key[r] != 0) << r;
     } else if (want > 0) {
-        uint32_t kth = 0;                                // the want-th largest key
-        for (int bit = 31; bit >= 0; --bit) {
+        // the want-th largest key: bit by bit, from the first in which two keys differ
+        uint32_t most = 0, least = ~0u;
+#pragma unroll
+        for (int r = 0; r < PER; ++r) {
+            most = max(most, key[r]);
+            if (key[r]) least = min(least, key[r]);
+        }
+        least = lowest(least);
+        most = ~lowest(~most);
+        const int bits = 32 - __clz(least ^ most);
+        uint32_t kth = bits == 32 ? 0 : (most >> bits) << bits;
+        for (int bit = bits - 1; bit >= 0; --bit) {
             const uint32_t cand = kth | (1u << bit);
             int n = 0;
 #pragma unroll
             for (int r = 0; r < PER; ++r) n += key[r] >= cand;
-            if (total(n) >= want) kth = cand;
+            n = total(n);
+            if (n >= want) kth = cand;
+            if (n == want) {                             // it is the least of these
+                uint32_t low = ~0u;
+#pragma unroll
+                for (int r = 0; r < PER; ++r)
+                    if (key[r] >= cand) low = min(low, key[r]);
+                kth = lowest(low);
+                break;
+            }
         }
         const float s = key_value(kth);
         const float above = s + 2.0f * err, below = s - 2.0f * err;
@@ -716,6 +761,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     // ---- exact keys of the undecided pages, in page order
     unsigned long long kth = 0;
     int ties = 0;
+    unsigned picked = 0;          // of up to 32 undecided pages
     if (unsure > need) {
         __syncwarp();
         if (kWarps > 1) __syncthreads();                 // all scores are in registers
@@ -763,16 +809,27 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
         }
         __syncwarp();
         if (kWarps > 1) __syncthreads();
-        // the need-th largest of them
-        for (int bit = 63; bit >= 0; --bit) {
-            const unsigned long long cand = kth | (1ull << bit);
+        if (unsure <= 32) {
+            // rank them against each other: lane i holds the i-th
+            const unsigned long long mine = lane < unsure ? exact[lane] : 0;
+            int ahead = 0;
+            for (int i = 0; i < unsure; ++i) {
+                const unsigned long long o = __shfl_sync(0xffffffffu, mine, i);
+                ahead += o > mine || (o == mine && i < lane);
+            }
+            picked = __ballot_sync(0xffffffffu, lane < unsure && ahead < need);
+        } else {
+            // the need-th largest of them
+            for (int bit = 63; bit >= 0; --bit) {
+                const unsigned long long cand = kth | (1ull << bit);
+                int n = 0;
+                for (int i = tid; i < unsure; i += THREADS) n += exact[i] >= cand;
+                if (total(n) >= need) kth = cand;
+            }
             int n = 0;
-            for (int i = tid; i < unsure; i += THREADS) n += exact[i] >= cand;
-            if (total(n) >= need) kth = cand;
+            for (int i = tid; i < unsure; i += THREADS) n += exact[i] > kth;
+            ties = need - total(n);                      // of the equal ones, from the lowest page up
         }
-        int n = 0;
-        for (int i = tid; i < unsure; i += THREADS) n += exact[i] > kth;
-        ties = need - total(n);                          // of the equal ones, from the lowest page up
     }
     // ---- the chosen pages in ascending order
     int at = 0, base = 0;
@@ -783,12 +840,16 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
             const bool open = (maybe >> r) & 1;
             int all;
             const int place = base + rank(open, all);
-            const unsigned long long k = open ? exact[place] : 0;
-            int equal;
-            const int eq = rank(open && k == kth, equal);
-            take = take || (open && (k > kth || (k == kth && eq < ties)));
-            ties = max(0, ties - equal);
             base += all;
+            if (unsure <= 32) {
+                take = take || (open && ((picked >> place) & 1));
+            } else {
+                const unsigned long long k = open ? exact[place] : 0;
+                int equal;
+                const int eq = rank(open && k == kth, equal);
+                take = take || (open && (k > kth || (k == kth && eq < ties)));
+                ties = max(0, ties - equal);
+            }
         }
         int all;
         const int pos = at + rank(take, all);
