@@ -518,34 +518,40 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
         float best = -INFINITY;       // G > ROWS: of this thread's page, over the rounds
         for (int r0 = 0; r0 < rows; r0 += ROWS) {
             __syncthreads();          // (the last reads of A, scores and sums)
-            if (tid < ROWS) s_sum[tid] = 0.f;
-            __syncthreads();
-            for (int i = tid; i < ROWS * (kChunks / 2); i += kScoreThreads) {
-                const int row = i / (kChunks / 2), c = i - row * (kChunks / 2);
-                uint4 x = make_uint4(0, 0, 0, 0);
+            constexpr int kHalf = kChunks / 2, kLoads = ROWS * kHalf / kScoreThreads;
+            uint4 x[kLoads];       // all in flight before the first is used
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const int row = tid / kHalf + k * (kScoreThreads / kHalf);
+                x[k] = make_uint4(0, 0, 0, 0);
                 if (r0 + row < rows) {
                     const int tk = (r0 + row) / p.G, h = r0 + row - tk * p.G;
-                    x = __ldg(reinterpret_cast<const uint4*>(
-                                  p.q + (size_t)(s0 + tk) * p.q_stride + (size_t)(hk * p.G + h) * D) + c);
+                    x[k] = __ldg(reinterpret_cast<const uint4*>(
+                                     p.q + (size_t)(s0 + tk) * p.q_stride +
+                                     (size_t)(hk * p.G + h) * D) + tid % kHalf);
                 }
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            }
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const int row = tid / kHalf + k * (kScoreThreads / kHalf), c = tid % kHalf;
+                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
                 uint32_t neg[4], pos[4];
                 float sum = 0.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float a = bf16_lo(w[k]), b = bf16_hi(w[k]);
+                for (int j = 0; j < 4; ++j) {
+                    const float a = bf16_lo(w[j]), b = bf16_hi(w[j]);
                     sum = fmaf(a, a, fmaf(b, b, sum));
                     // (a NaN goes with the negative part)
                     const uint32_t keep = (a >= 0.f ? 0x0000FFFFu : 0u) | (b >= 0.f ? 0xFFFF0000u : 0u);
-                    pos[k] = w[k] & keep;
-                    neg[k] = w[k] & ~keep;
+                    pos[j] = w[j] & keep;
+                    neg[j] = w[j] & ~keep;
                 }
                 *reinterpret_cast<uint4*>(sA + at(row, c)) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
-                *reinterpret_cast<uint4*>(sA + at(row, c + kChunks / 2)) =
+                *reinterpret_cast<uint4*>(sA + at(row, c + kHalf)) =
                     make_uint4(pos[0], pos[1], pos[2], pos[3]);
                 // the row's threads are neighbours in a warp
 #pragma unroll
-                for (int off = 1; off < kChunks / 2; off <<= 1)
+                for (int off = 1; off < kHalf; off <<= 1)
                     sum += __shfl_xor_sync(0xffffffffu, sum, off);
                 if (c == 0) s_sum[row] = sum;
             }
@@ -559,7 +565,7 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[n][k] = 0.f;
             const uint32_t a0 = smem_addr(sA), b0 = smem_addr(sB);
-#pragma unroll 4
+#pragma unroll 8
             for (int kk = 0; kk < kTerms / 16; ++kk) {
                 uint32_t a[4];
                 ldmatrix_x4(a0 + at(wr + (lane & 15), 2 * kk + (lane >> 4)), a);
