@@ -226,6 +226,7 @@ __device__ __forceinline__ uint32_t bf2_max_nan(uint32_t a, uint32_t b) {
 // Block (x, h): rows [x * ROWS, + ROWS) of head h.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const AppendParams p) {
+    static_assert(ROWS <= 32, "a warp looks at all of a block's rows");
     constexpr int kPieces = D / 8;                        // 16-byte pieces of a row
     constexpr int kSlots = kAppendThreads / kPieces;      // rows per pass
     __shared__ uint4 s_red[2][kAppendThreads / 32][kPieces];
@@ -271,17 +272,23 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
             }
     }
     if (p.bounds) {
-        for (int t = t0; t < t1; ++t) {
-            const long long s = slot_of(t);
-            if (s < 0) continue;
-            if (t + 1 < p.T) {
-                const long long nx = __ldg(p.slot_map + t + 1);
-                if (nx >= 0 && (nx >> p.page_shift) == (s >> p.page_shift)) continue;
-            }
-            // row t ends its page's run: reduce the page's slots 0 .. s % ps
+        // the rows that end their page's run (ROWS <= 32: each warp finds all of them)
+        unsigned ends;
+        {
+            const int t = t0 + lane;
+            const long long s = t < t1 ? slot_of(t) : -1;
+            const long long nx = t + 1 < p.T && t < t1 ? __ldg(p.slot_map + t + 1) : -1;
+            ends = __ballot_sync(0xffffffffu, s >= 0 && (nx < 0 || (nx >> p.page_shift) !=
+                                                                       (s >> p.page_shift)));
+        }
+        for (; ends; ends &= ends - 1) {
+            // reduce the page's slots 0 .. s % ps
+            const int t = t0 + __ffs(ends) - 1;
+            const long long s = __ldg(p.slot_map + t);
             const int last = (int)(s & (ps - 1));
             uint4 lo, hi;
             bool any = false;
+#pragma unroll 4
             for (int r = rs; r <= last; r += kSlots) {
                 const int u = t - (last - r);
                 const long long want = s - (last - r);
