@@ -297,29 +297,48 @@ def attn_bwd(q, k, v, o, dout, lse, dq, dk, dv, causal: bool, scale: float, work
 
 
 # ---- serving on a paged cache. These calls run on the device of their tensors,
-# whichever is current, on `stream` or that device's current stream.
+# whichever is current, on `stream` or that device's current stream. A step makes several of
+# them on small tensors, so the checks take one pass over the arguments.
 
-def _on_device(fn, what: str, tensors, args, stream) -> None:
+def _pointers(what: str, names: str, dtypes, tensors):
+    """The tensors' common device and their data pointers; refuses what the calls do not take."""
+    try:
+        dev = tensors[0].get_device()
+        for t, dtype in zip(tensors, dtypes):
+            if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+                break
+        else:
+            if dev >= 0:
+                return dev, [t.data_ptr() for t in tensors]
+    except AttributeError:
+        pass
     import torch
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev or dev < 0:
+    for name, t, dtype in zip(names.split(), tensors, dtypes):   # say which one
+        _tensor(t, dtype, f"{what}: {name}")
+        if not isinstance(t, torch.Tensor) or t.get_device() != tensors[0].get_device():
             raise ValueError(f"{what}: all tensors must be on one CUDA device")
+    raise ValueError(f"{what}: all tensors must be on one CUDA device")
+
+
+def _launch(fn, what: str, dev: int, args, stream) -> None:
+    import torch
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            code = fn(*args, _stream(stream))
-    else:
-        code = fn(*args, _stream(stream))
-    _check(code, what)
+            return _launch(fn, what, dev, args, stream)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev).cuda_stream, sooner
+    code = fn(*args, int(stream))
+    if code != ATTN_OK:
+        raise AttnError(code, what)
 
 
-def _rows(t, name: str):
-    """Pointer and row stride of a bf16 [T, H, d] tensor whose rows are dense."""
+def _rows(t, name: str, dev: int):
+    """Pointer and row stride of a bf16 [T, H, d] tensor on device `dev` whose rows are dense."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
-        raise ValueError(f"{name} must be a 3-D CUDA tensor of torch.bfloat16")
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D tensor of torch.bfloat16 on the others' device")
     T, H, d = t.shape
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != d and H > 1):
@@ -334,23 +353,22 @@ def attn_page_tables(ctx_lens, new_lens, free_pages, free_head, free_head_out, b
     free_head_out [1], block_table [B,max_pages], cu_q [B+1] int32; slot_map [T] int64.
     free_head_out may be free_head, and seq_lens may be ctx_lens."""
     import torch
-    B = ctx_lens.shape[0]
-    if ctx_lens.dim() != 1 or tuple(new_lens.shape) != (B,) or tuple(seq_lens.shape) != (B,) \
-            or tuple(cu_q.shape) != (B + 1,) or block_table.dim() != 2 \
-            or block_table.shape[0] != B or free_pages.dim() != 1 or slot_map.dim() != 1 \
-            or free_head.numel() != 1 or free_head_out.numel() != 1:
-        raise ValueError("attn_page_tables: inconsistent shapes")
     i32 = torch.int32
-    _on_device(lib.attn_page_tables, "attn_page_tables",
-               (ctx_lens, new_lens, free_pages, free_head, free_head_out, block_table, seq_lens,
-                cu_q, slot_map),
-               (_tensor(ctx_lens, i32, "ctx_lens"), _tensor(new_lens, i32, "new_lens"),
-                _tensor(free_pages, i32, "free_pages"), _tensor(free_head, i32, "free_head"),
-                _tensor(free_head_out, i32, "free_head_out"),
-                _tensor(block_table, i32, "block_table"), _tensor(seq_lens, i32, "seq_lens"),
-                _tensor(cu_q, i32, "cu_q"), _tensor(slot_map, torch.int64, "slot_map"), B,
-                slot_map.shape[0], free_pages.shape[0], int(page_size), block_table.shape[1],
-                int(num_pages)), stream)
+    dev, ptrs = _pointers(
+        "attn_page_tables",
+        "ctx_lens new_lens free_pages free_head free_head_out block_table seq_lens cu_q slot_map",
+        (i32, i32, i32, i32, i32, i32, i32, i32, torch.int64),
+        (ctx_lens, new_lens, free_pages, free_head, free_head_out, block_table, seq_lens, cu_q,
+         slot_map))
+    B = ctx_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or ctx_lens.shape != (B,) \
+            or new_lens.shape != (B,) or seq_lens.shape != (B,) or cu_q.shape != (B + 1,) \
+            or free_pages.dim() != 1 or slot_map.dim() != 1 or free_head.numel() != 1 \
+            or free_head_out.numel() != 1:
+        raise ValueError("attn_page_tables: inconsistent shapes")
+    _launch(lib.attn_page_tables, "attn_page_tables", dev,
+            (*ptrs, B, slot_map.numel(), free_pages.numel(), int(page_size),
+             block_table.shape[1], int(num_pages)), stream)
 
 
 def attn_paged_append(k, v, slot_map, k_cache, v_cache, k_bounds=None, stream=None) -> None:
@@ -359,24 +377,39 @@ def attn_paged_append(k, v, slot_map, k_cache, v_cache, k_bounds=None, stream=No
     [num_pages,Hkv,2,d] bf16 or None."""
     import torch
     bf16 = torch.bfloat16
-    kp, ks = _rows(k, "k")
-    vp, vs = _rows(v, "v")
+    if k_bounds is None:
+        dev, ptrs = _pointers("attn_paged_append", "slot_map k_cache v_cache",
+                              (torch.int64, bf16, bf16), (slot_map, k_cache, v_cache))
+        ptrs.append(None)
+    else:
+        dev, ptrs = _pointers("attn_paged_append", "slot_map k_cache v_cache k_bounds",
+                              (torch.int64, bf16, bf16, bf16),
+                              (slot_map, k_cache, v_cache, k_bounds))
+    kp, ks = _rows(k, "k", dev)
+    vp, vs = _rows(v, "v", dev)
     T, Hkv, d = k.shape
+    if k_cache.dim() != 4:
+        raise ValueError("attn_paged_append: inconsistent shapes")
     P, H2, page_size, d2 = k_cache.shape
     if v.shape != k.shape or vs != ks or H2 != Hkv or d2 != d or v_cache.shape != k_cache.shape \
-            or tuple(slot_map.shape) != (T,) \
-            or (k_bounds is not None and tuple(k_bounds.shape) != (P, Hkv, 2, d)):
+            or slot_map.shape != (T,) \
+            or (k_bounds is not None and k_bounds.shape != (P, Hkv, 2, d)):
         raise ValueError("attn_paged_append: inconsistent shapes")
-    tensors = (k, v, slot_map, k_cache, v_cache) + (() if k_bounds is None else (k_bounds,))
-    _on_device(lib.attn_paged_append, "attn_paged_append", tensors,
-               (kp, vp, _tensor(slot_map, torch.int64, "slot_map"),
-                _tensor(k_cache, bf16, "k_cache"), _tensor(v_cache, bf16, "v_cache"),
-                None if k_bounds is None else _tensor(k_bounds, bf16, "k_bounds"), T, Hkv, d, ks,
-                page_size, P), stream)
+    _launch(lib.attn_paged_append, "attn_paged_append", dev,
+            (kp, vp, *ptrs, T, Hkv, d, ks, page_size, P), stream)
 
 
 def attn_fwd_paged_workspace_bytes(d: int) -> int:
     return int(lib.attn_fwd_paged_workspace_bytes(d))
+
+
+def _check_step(what: str, q, block_table, cu_q, seq_lens) -> int:
+    """The number of sequences, once the shapes that all calls on q share agree."""
+    B = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or cu_q.shape != (B + 1,) \
+            or seq_lens.dim() != 1:
+        raise ValueError(f"{what}: inconsistent shapes")
+    return B
 
 
 def attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, seq_lens, o, lse, causal: bool,
@@ -386,22 +419,20 @@ def attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, seq_lens, o, lse, cau
     int32; o [T,Hq,d] bf16, lse [T,Hq] fp32; workspace: uint8, attn_fwd_paged_workspace_bytes(d)."""
     import torch
     bf16, i32 = torch.bfloat16, torch.int32
-    qp, qs = _rows(q, "q")
+    dev, ptrs = _pointers("attn_fwd_paged",
+                          "k_cache v_cache block_table cu_q seq_lens o lse workspace",
+                          (bf16, bf16, i32, i32, i32, bf16, torch.float32, torch.uint8),
+                          (k_cache, v_cache, block_table, cu_q, seq_lens, o, lse, workspace))
+    qp, qs = _rows(q, "q", dev)
     T, Hq, d = q.shape
-    P, Hkv, page_size, d2 = k_cache.shape
-    B = seq_lens.shape[0]
-    if d2 != d or v_cache.shape != k_cache.shape or block_table.dim() != 2 \
-            or block_table.shape[0] != B or tuple(cu_q.shape) != (B + 1,) or seq_lens.dim() != 1 \
-            or o.shape != q.shape or tuple(lse.shape) != (T, Hq):
+    B = _check_step("attn_fwd_paged", q, block_table, cu_q, seq_lens)
+    if k_cache.dim() != 4 or k_cache.shape[3] != d or v_cache.shape != k_cache.shape \
+            or o.shape != q.shape or lse.shape != (T, Hq):
         raise ValueError("attn_fwd_paged: inconsistent shapes")
-    _on_device(lib.attn_fwd_paged, "attn_fwd_paged",
-               (q, k_cache, v_cache, block_table, cu_q, seq_lens, o, lse, workspace),
-               (qp, _tensor(k_cache, bf16, "k_cache"), _tensor(v_cache, bf16, "v_cache"),
-                _tensor(block_table, i32, "block_table"), _tensor(cu_q, i32, "cu_q"),
-                _tensor(seq_lens, i32, "seq_lens"), _tensor(o, bf16, "o"),
-                _tensor(lse, torch.float32, "lse"), B, T, Hq, Hkv, d, qs, page_size,
-                block_table.shape[1], P, int(bool(causal)), float(scale),
-                _tensor(workspace, torch.uint8, "workspace"), workspace.numel()), stream)
+    P, Hkv, page_size, _ = k_cache.shape
+    _launch(lib.attn_fwd_paged, "attn_fwd_paged", dev,
+            (qp, *ptrs[:7], B, T, Hq, Hkv, d, qs, page_size, block_table.shape[1], P,
+             1 if causal else 0, scale, ptrs[7], workspace.numel()), stream)
 
 
 def attn_page_select_workspace_bytes(T: int, Hkv: int, max_pages: int) -> int:
@@ -415,22 +446,19 @@ def attn_page_select(q, k_bounds, block_table, cu_q, seq_lens, sel, page_size: i
     [B], sel [T,Hkv,K] int32; workspace: uint8, attn_page_select_workspace_bytes(...)."""
     import torch
     i32 = torch.int32
-    qp, qs = _rows(q, "q")
+    dev, ptrs = _pointers("attn_page_select", "k_bounds block_table cu_q seq_lens sel workspace",
+                          (torch.bfloat16, i32, i32, i32, i32, torch.uint8),
+                          (k_bounds, block_table, cu_q, seq_lens, sel, workspace))
+    qp, qs = _rows(q, "q", dev)
     T, Hq, d = q.shape
-    P, Hkv, two, d2 = k_bounds.shape
-    B = seq_lens.shape[0]
-    if two != 2 or d2 != d or block_table.dim() != 2 or block_table.shape[0] != B \
-            or tuple(cu_q.shape) != (B + 1,) or seq_lens.dim() != 1 or sel.dim() != 3 \
-            or tuple(sel.shape[:2]) != (T, Hkv):
+    B = _check_step("attn_page_select", q, block_table, cu_q, seq_lens)
+    if k_bounds.dim() != 4 or k_bounds.shape[2:] != (2, d) or sel.dim() != 3 \
+            or sel.shape[:2] != (T, k_bounds.shape[1]):
         raise ValueError("attn_page_select: inconsistent shapes")
-    _on_device(lib.attn_page_select, "attn_page_select",
-               (q, k_bounds, block_table, cu_q, seq_lens, sel, workspace),
-               (qp, _tensor(k_bounds, torch.bfloat16, "k_bounds"),
-                _tensor(block_table, i32, "block_table"), _tensor(cu_q, i32, "cu_q"),
-                _tensor(seq_lens, i32, "seq_lens"), _tensor(sel, i32, "sel"), B, T, Hq, Hkv, d,
-                sel.shape[2], int(keep_first), int(keep_last), qs, int(page_size),
-                block_table.shape[1], P, _tensor(workspace, torch.uint8, "workspace"),
-                workspace.numel()), stream)
+    _launch(lib.attn_page_select, "attn_page_select", dev,
+            (qp, *ptrs[:5], B, T, Hq, k_bounds.shape[1], d, sel.shape[2], int(keep_first),
+             int(keep_last), qs, int(page_size), block_table.shape[1], k_bounds.shape[0], ptrs[5],
+             workspace.numel()), stream)
 
 
 def attn_sparse_paged(q, k_cache, v_cache, block_table, cu_q, seq_lens, sel, o, lse,
@@ -438,23 +466,21 @@ def attn_sparse_paged(q, k_cache, v_cache, block_table, cu_q, seq_lens, sel, o, 
     """attn_fwd_paged (causal) over the pages listed in sel [T,Hkv,K] int32 (-1: none)."""
     import torch
     bf16, i32 = torch.bfloat16, torch.int32
-    qp, qs = _rows(q, "q")
+    dev, ptrs = _pointers("attn_sparse_paged",
+                          "k_cache v_cache block_table cu_q seq_lens sel o lse workspace",
+                          (bf16, bf16, i32, i32, i32, i32, bf16, torch.float32, torch.uint8),
+                          (k_cache, v_cache, block_table, cu_q, seq_lens, sel, o, lse, workspace))
+    qp, qs = _rows(q, "q", dev)
     T, Hq, d = q.shape
-    P, Hkv, page_size, d2 = k_cache.shape
-    B = seq_lens.shape[0]
-    if d2 != d or v_cache.shape != k_cache.shape or block_table.dim() != 2 \
-            or block_table.shape[0] != B or tuple(cu_q.shape) != (B + 1,) or seq_lens.dim() != 1 \
-            or o.shape != q.shape or tuple(lse.shape) != (T, Hq) or sel.dim() != 3 \
-            or tuple(sel.shape[:2]) != (T, Hkv):
+    B = _check_step("attn_sparse_paged", q, block_table, cu_q, seq_lens)
+    if k_cache.dim() != 4 or k_cache.shape[3] != d or v_cache.shape != k_cache.shape \
+            or o.shape != q.shape or lse.shape != (T, Hq) or sel.dim() != 3 \
+            or sel.shape[:2] != (T, k_cache.shape[1]):
         raise ValueError("attn_sparse_paged: inconsistent shapes")
-    _on_device(lib.attn_sparse_paged, "attn_sparse_paged",
-               (q, k_cache, v_cache, block_table, cu_q, seq_lens, sel, o, lse, workspace),
-               (qp, _tensor(k_cache, bf16, "k_cache"), _tensor(v_cache, bf16, "v_cache"),
-                _tensor(block_table, i32, "block_table"), _tensor(cu_q, i32, "cu_q"),
-                _tensor(seq_lens, i32, "seq_lens"), _tensor(sel, i32, "sel"),
-                _tensor(o, bf16, "o"), _tensor(lse, torch.float32, "lse"), B, T, Hq, Hkv, d,
-                sel.shape[2], qs, page_size, block_table.shape[1], P, float(scale),
-                _tensor(workspace, torch.uint8, "workspace"), workspace.numel()), stream)
+    P, Hkv, page_size, _ = k_cache.shape
+    _launch(lib.attn_sparse_paged, "attn_sparse_paged", dev,
+            (qp, *ptrs[:8], B, T, Hq, Hkv, d, sel.shape[2], qs, page_size, block_table.shape[1], P,
+             scale, ptrs[8], workspace.numel()), stream)
 
 
 def attn_status(stream=None) -> int:

@@ -849,7 +849,10 @@ attn_status_t attn_page_tables(const int* ctx_lens, const int* new_lens, const i
         if (!g_dev[dev].tables_attr_set) {
             if (cudaFuncSetAttribute(attn_page_tables_kernel,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (3 * kTablesMaxSeqs + 1) * 4) != cudaSuccess)
+                                     (3 * kTablesMaxSeqs + 1) * 4) != cudaSuccess ||
+                cudaFuncSetAttribute(attn_page_tables_kernel,
+                                     cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                     1) != cudaSuccess)
                 return ATTN_ERR_CUDA;
             g_dev[dev].tables_attr_set = true;
         }
@@ -857,7 +860,11 @@ attn_status_t attn_page_tables(const int* ctx_lens, const int* new_lens, const i
     TablesParams p{ctx_lens, new_lens,  free_pages, free_head, free_head_out,
                    block_table, seq_lens, cu_q,     slot_map,  B,
                    T,        num_free,  shift_of(page_size), max_pages_per_seq, num_pages};
-    const int ctas = T <= kTablesThreads ? 1 : T <= 2 * kTablesThreads ? 2 : 8;
+    // as many CTAs as there are rows for, up to the largest cluster
+    const int ctas = T <= kTablesThreads       ? 1
+                     : T <= 2 * kTablesThreads ? 2
+                     : T <= 8 * kTablesThreads ? 8
+                                               : 16;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kTablesThreads);

