@@ -173,26 +173,26 @@ struct PagedUnit {
 };
 static_assert(sizeof(PagedUnit) == 64, "unit record");
 
-// Waits of the roles. Where few registers are live (N > 0) the part that actually waits is
-// one function for all of them: some thirty copies of it, inlined, kept the SM's
-// instruction cache (shared by roles that run different code at the same time) from
-// holding their loops.
+// Waits of the roles. The part that actually waits is one function for all of them: some
+// thirty copies of it, inlined, kept the SM's instruction cache (shared by roles that run
+// different code at the same time) from holding their loops. Only the softmax warps of
+// the 128-row form, with a row of scores in registers, have it inline (SLIM = false).
 __device__ __noinline__ bool paged_wait_slow(uint32_t bar, uint32_t parity,
                                              volatile int* abort_flag) {
     return mbar_wait_limit(bar, parity, abort_flag, &g_attn_status, kWaitLimitNs);
 }
-template <class T>
+template <bool SLIM = true>
 __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity,
                                            volatile int* abort_flag) {
-    if constexpr (T::kN == 0) return mbar_wait(bar, parity, abort_flag, &g_attn_status);
+    if constexpr (!SLIM) return mbar_wait(bar, parity, abort_flag, &g_attn_status);
     if (mbar_test(bar, parity)) return true;
     return paged_wait_slow(bar, parity, abort_flag);
 }
 // by a whole warp; the outcome is the same in all lanes
-template <class T>
+template <bool SLIM = true>
 __device__ __forceinline__ bool paged_warp_wait(uint32_t bar, uint32_t parity,
                                                 volatile int* abort_flag) {
-    const bool ok = paged_wait<T>(bar, parity, abort_flag);
+    const bool ok = paged_wait<SLIM>(bar, parity, abort_flag);
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -451,7 +451,7 @@ __device__ void paged_planner(const PagedParams& p, const PagedStretch& st, cons
             if (visible(ahead_e)) ahead_page = page_of(ahead_e);
         }
         if (units >= (uint32_t)T::kUnits &&
-            !paged_warp_wait<T>(b.unit_empty(ri), (units / T::kUnits - 1) & 1, sh.abort_flag))
+            !paged_warp_wait(b.unit_empty(ri), (units / T::kUnits - 1) & 1, sh.abort_flag))
             return;
         if (more) {
             const long long ulen = w.line.unit(w.q);
@@ -583,7 +583,7 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
 
     for (uint32_t units = 0;; ++units) {
         const int ri = units % T::kUnits;
-        if (!paged_warp_wait<T>(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag)) goto fail;
+        if (!paged_warp_wait(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag)) goto fail;
         {
             const volatile PagedUnit& u = ring[ri];
             const int kind = u.kind;
@@ -599,7 +599,7 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
                 for (int t = 0; t < (wide ? 2 : 1); ++t) {
                     const int slot = wide ? t : uqs;
                     if (q_used[slot] > 0 &&
-                        !paged_warp_wait<T>(b.q_empty(slot), (q_used[slot] - 1) & 1, abort_flag))
+                        !paged_warp_wait(b.q_empty(slot), (q_used[slot] - 1) & 1, abort_flag))
                         goto fail;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(b.q_full(slot),
@@ -651,7 +651,7 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
                 const uint32_t pair = it % T::kPairs, round = it / T::kPairs;
                 const uint32_t sk = 2 * pair, sv = 2 * pair + 1;
                 if constexpr (K) {
-                    if (round > 0 && !paged_warp_wait<T>(b.kv_empty(sk), (round - 1) & 1, abort_flag))
+                    if (round > 0 && !paged_warp_wait(b.kv_empty(sk), (round - 1) & 1, abort_flag))
                         goto fail;
                     if (lane < 4)
                         reinterpret_cast<volatile uint32_t*>(
@@ -667,7 +667,7 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
                                          panel * 64, y, z, pol);
                 }
                 if constexpr (V) {
-                    if (round > 0 && !paged_warp_wait<T>(b.kv_empty(sv), (round - 1) & 1, abort_flag)) {
+                    if (round > 0 && !paged_warp_wait(b.kv_empty(sv), (round - 1) & 1, abort_flag)) {
                         ++it;   // this tile's V is not in flight
                         raw_last |= 1u << (8 + pair);
                         goto fail;
@@ -676,7 +676,7 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
                     if (!whole) {   // rows without a key must be zeroed before P V
                         const uint32_t i = tails & 1;
                         if (tails >= 2 &&
-                            !paged_warp_wait<T>(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) {
+                            !paged_warp_wait(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) {
                             ++it;
                             raw_last |= 1u << (8 + pair);
                             goto fail;
@@ -713,7 +713,7 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
     }
     if (V) {
         const uint32_t i = tails & 1;
-        if (tails >= 2 && !paged_warp_wait<T>(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) goto fail;
+        if (tails >= 2 && !paged_warp_wait(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) goto fail;
         if (lane == 0) {
             reinterpret_cast<volatile int*>(sh.tail_info)[i] = -1;
             mbar_arrive(b.tail_full(i));
@@ -728,17 +728,17 @@ fail:
         const uint32_t first = it > (uint32_t)T::kPairs ? it - T::kPairs : 0;
         for (uint32_t i = first; i < it; ++i) {
             const uint32_t pair = i % T::kPairs, par = (i / T::kPairs) & 1;
-            if (K) paged_wait<T>(b.kv_full(2 * pair), par, &no_abort);
+            if (K) paged_wait(b.kv_full(2 * pair), par, &no_abort);
             const bool no_v = i + 1 == it && ((raw_last >> (8 + pair)) & 1);
             if (!V || no_v) continue;
             if ((raw_last >> pair) & 1)
-                paged_wait<T>(b.v_raw(pair), ((raw_par >> pair) & 1) ^ 1, &no_abort);
+                paged_wait(b.v_raw(pair), ((raw_par >> pair) & 1) ^ 1, &no_abort);
             else
-                paged_wait<T>(b.kv_full(2 * pair + 1), par, &no_abort);
+                paged_wait(b.kv_full(2 * pair + 1), par, &no_abort);
         }
         for (int i = 0; i < 2; ++i)
             if (K && q_used[i] > 0)
-                paged_wait<T>(b.q_full(i), (q_used[i] - 1) & 1, &no_abort);
+                paged_wait(b.q_full(i), (q_used[i] - 1) & 1, &no_abort);
     }
     __syncwarp();
 }
@@ -749,11 +749,11 @@ __device__ void paged_tail(const PagedBars<T>& b, const PagedShared& sh, int lan
     const uint32_t sKV = smem_addr(sh.smem) + T::kOffKV;
     uint32_t par = 0;
     for (uint32_t i = 0;; ++i) {
-        if (!paged_warp_wait<T>(b.tail_full(i & 1), (i >> 1) & 1, sh.abort_flag)) return;
+        if (!paged_warp_wait(b.tail_full(i & 1), (i >> 1) & 1, sh.abort_flag)) return;
         const int info = reinterpret_cast<volatile int*>(sh.tail_info)[i & 1];
         if (info < 0) return;
         const uint32_t pair = info;
-        if (!paged_warp_wait<T>(b.v_raw(pair), (par >> pair) & 1, sh.abort_flag)) return;
+        if (!paged_warp_wait(b.v_raw(pair), (par >> pair) & 1, sh.abort_flag)) return;
         par ^= 1u << pair;
         const volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(sh.tail_mask) + 4 * (i & 1);
         const uint32_t tile = sKV + (2 * pair + 1) * T::kTileBytes;
@@ -793,7 +793,7 @@ __device__ void paged_mma(uint32_t tbase, const PagedBars<PagedTraits<D>>& b,
     uint32_t it = 0, units = 0;
     uint32_t q_used[2] = {0, 0}, o_used[2] = {0, 0}, p_par[2] = {0, 0};
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return paged_wait<T>(bar, parity, abort_flag);
+        return paged_wait(bar, parity, abort_flag);
     };
     for (;; ++units) {
         const int ri = units % T::kUnits;
@@ -810,62 +810,60 @@ __device__ void paged_mma(uint32_t tbase, const PagedBars<PagedTraits<D>>& b,
         const int steps = max(n[0], n[1]);
         for (int t = 0; t < (wide ? 2 : 1); ++t) {
             const int slot = wide ? t : uqs;
-            if (!wait(b.q_full(slot), q_used[slot] & 1)) goto done;
-            ++q_used[slot];
+            const uint32_t used = slot ? q_used[1] : q_used[0];
+            if (!wait(b.q_full(slot), used & 1)) goto done;
+            if (slot) ++q_used[1];
+            else ++q_used[0];
+            if (wide && (t ? n[1] : n[0]) == 0) mma_commit_w(b.q_empty(t), 1);
         }
-        const uint64_t dq[2] = {dq0 + (wide ? 0 : uqs) * kTileStep,
-                                dq0 + (wide ? 1 : uqs) * kTileStep};
-        // key tile k of the unit sits in pair (it + k) % kPairs
-        auto issue_s = [&](int t, int i) -> bool {
-            const int k = wide ? i : 2 * i + t;
-            const uint32_t x = it + k, sk = 2 * (x % T::kPairs);
-            // (tile 1 of a wide unit finds what tile 0 has waited for)
-            if (!(wide && t == 1 && i < n[0]) && !wait(b.kv_full(sk), (x / T::kPairs) & 1))
-                return false;
-            tc_fence_after_sync();
-            fwd_issue_s<D, false>(tbase + (t ? T::kColS1 : T::kColS0), dq[t], dk0 + sk * kTileStep, 1);
-            mma_commit_w(b.s_full(t), 1);
-            if (!wide || t == 1 || i >= n[1]) mma_commit_w(b.kv_empty(sk), 1);
-            // a Q tile's last product lets the producer refill it
-            if (wide ? i == n[t] - 1 : k == N - 1) mma_commit_w(b.q_empty(wide ? t : uqs), 1);
-            return true;
-        };
-        auto issue_pv = [&](int t, int i) -> bool {
-            const int k = wide ? i : 2 * i + t;
-            const uint32_t x = it + k, sv = 2 * (x % T::kPairs) + 1;
-            if (!(wide && t == 1 && i < n[0]) && !wait(b.kv_full(sv), (x / T::kPairs) & 1))
-                return false;
-            if (!wait(b.p_full(t), p_par[t])) return false;
-            p_par[t] ^= 1;
-            if (i == 0 && o_used[t] > 0 && !wait(b.o_free(t), (o_used[t] - 1) & 1)) return false;
-            tc_fence_after_sync();
-            const uint32_t tO = tbase + (t ? T::kColO1 : T::kColO0);
-            const uint32_t tP = tbase + (t ? T::kColS1 : T::kColS0);
-            fwd_issue_pv<D, false>(tO, tP, dv0 + sv * kTileStep, i > 0, 0, 1);
-            fwd_issue_pv<D, false>(tO, tP, dv0 + sv * kTileStep, true, 1, 1);
-            if (i == n[t] - 1) mma_commit_w(b.o_final(t), 1);
-            if (!wide || t == 1 || i >= n[1]) mma_commit_w(b.kv_empty(sv), 1);
-            return true;
-        };
-        for (int t = 0; t < 2; ++t) {
-            if (n[t] > 0 && !issue_s(t, 0)) goto done;
-            if (wide && n[t] == 0) mma_commit_w(b.q_empty(t), 1);
-        }
-        for (int i = 0; i < steps; ++i) {
+        // key tile k of the unit sits in pair (it + k) % kPairs. One copy of each product's
+        // code serves both t (rolled loops: the roles share the instruction cache).
+#pragma unroll 1
+        for (int i = -1; i < steps; ++i) {
+#pragma unroll 1
             for (int t = 0; t < 2; ++t) {
-                if (i < n[t] && !issue_pv(t, i)) goto done;
-                if (i + 1 < n[t] && !issue_s(t, i + 1)) goto done;
+                const int nt = t ? n[1] : n[0];
+                const uint32_t tS = tbase + (t ? T::kColS1 : T::kColS0);
+                // tile 1 of a wide unit finds what tile 0 has waited for
+                const bool second = wide && t == 1;
+                if (i >= 0 && i < nt) {
+                    const uint32_t x = it + (wide ? i : 2 * i + t), sv = 2 * (x % T::kPairs) + 1;
+                    if (!(second && i < n[0]) && !wait(b.kv_full(sv), (x / T::kPairs) & 1)) goto done;
+                    const uint32_t par = t ? p_par[1] : p_par[0], used = t ? o_used[1] : o_used[0];
+                    if (!wait(b.p_full(t), par)) goto done;
+                    if (t) p_par[1] ^= 1;
+                    else p_par[0] ^= 1;
+                    if (i == 0 && used > 0 && !wait(b.o_free(t), (used - 1) & 1)) goto done;
+                    tc_fence_after_sync();
+                    const uint32_t tO = tbase + (t ? T::kColO1 : T::kColO0);
+                    fwd_issue_pv<D, false>(tO, tS, dv0 + sv * kTileStep, i > 0, 0, 1);
+                    fwd_issue_pv<D, false>(tO, tS, dv0 + sv * kTileStep, true, 1, 1);
+                    if (i == nt - 1) mma_commit_w(b.o_final(t), 1);
+                    if (!wide || t == 1 || i >= n[1]) mma_commit_w(b.kv_empty(sv), 1);
+                }
+                const int i1 = i + 1;
+                if (i1 < nt) {
+                    const int k = wide ? i1 : 2 * i1 + t;
+                    const uint32_t x = it + k, sk = 2 * (x % T::kPairs);
+                    if (!(second && i1 < n[0]) && !wait(b.kv_full(sk), (x / T::kPairs) & 1)) goto done;
+                    tc_fence_after_sync();
+                    fwd_issue_s<D, false>(tS, dq0 + (wide ? t : uqs) * kTileStep, dk0 + sk * kTileStep, 1);
+                    mma_commit_w(b.s_full(t), 1);
+                    if (!wide || t == 1 || i1 >= n[1]) mma_commit_w(b.kv_empty(sk), 1);
+                    // a Q tile's last product lets the producer refill it
+                    if (wide ? i1 == nt - 1 : k == N - 1) mma_commit_w(b.q_empty(wide ? t : uqs), 1);
+                }
             }
         }
-        for (int t = 0; t < 2; ++t)
-            if (n[t] > 0) ++o_used[t];
+        if (n[0] > 0) ++o_used[0];
+        if (n[1] > 0) ++o_used[1];
         it += N;
     }
 done: {
     // Every MMA issued so far must finish before tensor memory is released.
     volatile int no_abort = 0;
     mma_commit_w(b.drain(), 1);
-    paged_wait<T>(b.drain(), 0, &no_abort);
+    paged_wait(b.drain(), 0, &no_abort);
 }
 }
 
@@ -915,7 +913,7 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
 
     for (uint32_t units = 0;; ++units) {
         const int ri = units % T::kUnits;
-        if (!paged_warp_wait<T>(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag)) return;
+        if (!paged_warp_wait<false>(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag)) return;
         const volatile PagedUnit& uu = ring[ri];
         const int kind = uu.kind, hk = uu.hk, tok0 = uu.tok, ntok = uu.ntok, pos0 = uu.pos0;
         const int len = uu.len, key0 = uu.key0, un[2] = {uu.n0, uu.n1}, slot = uu.slot;
@@ -935,7 +933,7 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
 
         for (int i = 0; i < n; ++i) {
             const int k = wide ? i : 2 * i + t;
-            if (!paged_warp_wait<T>(b.s_full(t), s_cnt & 1, abort_flag)) return;
+            if (!paged_warp_wait<false>(b.s_full(t), s_cnt & 1, abort_flag)) return;
             ++s_cnt;
             if (!active) {   // no row to work on: P stays what it is (rows are independent)
                 __syncwarp();
@@ -945,7 +943,7 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
             // the mask was written before K was loaded, and its entry is not written again
             // before this tile's P V has freed V's slot
             const uint32_t x = it + k;
-            if (!paged_warp_wait<T>(b.mask_full(x % T::kMasks), (x / T::kMasks) & 1, abort_flag)) return;
+            if (!paged_warp_wait<false>(b.mask_full(x % T::kMasks), (x / T::kMasks) & 1, abort_flag)) return;
             const uint4 mask = ld_shared_v4(masks + 16 * (x % T::kMasks));
             tc_fence_after_sync();
             uint32_t sr[128];
@@ -1024,7 +1022,7 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
         // ---- epilogue
         const bool joins = !wide && un[1] > 0;   // group 0 joins both groups' results
         const bool used = n > 0;
-        if (used && !paged_warp_wait<T>(b.o_final(t), o_used[t] & 1, abort_flag)) return;
+        if (used && !paged_warp_wait<false>(b.o_final(t), o_used[t] & 1, abort_flag)) return;
         float w0 = 1.f, w1 = 0.f;
         if (joins) {
             if (t == 1) {
@@ -1034,8 +1032,8 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
                 if (lane == 0) mbar_arrive(b.ml_full(0));
             } else {
                 // group 1 has waited for its own o_final by then
-                if (!paged_warp_wait<T>(b.ml_full(0), ml_cnt & 1, abort_flag)) return;
-                if (!paged_warp_wait<T>(b.o_final(1), o_used[1] & 1, abort_flag)) return;
+                if (!paged_warp_wait<false>(b.ml_full(0), ml_cnt & 1, abort_flag)) return;
+                if (!paged_warp_wait<false>(b.o_final(1), o_used[1] & 1, abort_flag)) return;
                 const float m1 = ml[r].x, l1 = ml[r].y;
                 const float m = fmaxf(m_ref, m1);
                 const float mb = m == -INFINITY ? 0.f : m;

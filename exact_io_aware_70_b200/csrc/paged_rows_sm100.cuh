@@ -121,7 +121,7 @@ __device__ void rows_mma(uint32_t tbase, const PagedBars<PagedTraits<D, N>>& b,
     uint32_t it = 0, units = 0, o_used = 0, p_cnt = 0;
     uint32_t q_par[2] = {0, 0};
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return paged_wait<T>(bar, parity, abort_flag);
+        return paged_wait(bar, parity, abort_flag);
     };
     for (;; ++units) {
         const int ri = units % T::kUnits;
@@ -181,7 +181,7 @@ done: {
     // Every MMA this thread issued must finish before tensor memory is released.
     volatile int no_abort = 0;
     mma_commit(b.drain());
-    paged_wait<T>(b.drain(), 0, &no_abort);
+    paged_wait(b.drain(), 0, &no_abort);
 }
 }
 
@@ -226,7 +226,7 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
 
     for (uint32_t units = 0;; ++units) {
         const int ri = units % T::kUnits;
-        const bool got = paged_warp_wait<T>(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag);
+        const bool got = paged_warp_wait(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag);
         if (r < N) minus_ref[r] = FLT_MAX;
         if (group_any(t, !got)) return;
         const volatile PagedUnit& uu = ring[ri];
@@ -242,13 +242,13 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
         for (int c = 0; c < N; ++c) l[c] = 0.f;
         for (int i = 0; i < n; ++i) {
             const uint32_t x = it + 2 * i + t;
-            bool ok = paged_warp_wait<T>(b.mask_full(x % T::kMasks), (x / T::kMasks) & 1, abort_flag);
+            bool ok = paged_warp_wait(b.mask_full(x % T::kMasks), (x / T::kMasks) & 1, abort_flag);
             const bool there = (masks[4 * (x % T::kMasks) + quarter] >> lane) & 1;
             // rows [first, N) see this key
             const long long key = (long long)key0 + (2 * i + t) * 128 + r;
             const long long behind = diag ? key - pos0 : 0;   // tokens before the key's own
             const int first = !there ? N : behind <= 0 ? 0 : behind >= N ? N : (int)behind * p.G;
-            ok = ok && paged_warp_wait<T>(b.s_full(t), s_cnt & 1, abort_flag);
+            ok = ok && paged_warp_wait(b.s_full(t), s_cnt & 1, abort_flag);
             ++s_cnt;
             tc_fence_after_sync();
             // exponents of every column in use, and whether one of them is above 2^8
@@ -370,7 +370,7 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
                     if ((lane & 1) == 0) red[quarter * N + c0 + (lane >> 1)] = x;
                 }
             }
-            const bool ok = paged_warp_wait<T>(b.o_final(t), o_used[t] & 1, abort_flag);
+            const bool ok = paged_warp_wait(b.o_final(t), o_used[t] & 1, abort_flag);
             if (group_any(t, !ok)) return;
             if (r < N && r < rows) {
                 m = -minus_ref[r];
@@ -388,8 +388,8 @@ __device__ void rows_softmax(const PagedParams& p, uint32_t tbase,
         } else {
             if (both) {
                 // the other group has waited for its own o_final by then
-                const bool ok = paged_warp_wait<T>(b.ml_full(t), ml_cnt & 1, abort_flag) &&
-                                paged_warp_wait<T>(b.o_final(t ^ 1), o_used[t ^ 1] & 1, abort_flag);
+                const bool ok = paged_warp_wait(b.ml_full(t), ml_cnt & 1, abort_flag) &&
+                                paged_warp_wait(b.o_final(t ^ 1), o_used[t ^ 1] & 1, abort_flag);
                 if (group_any(t, !ok)) return;
                 ++ml_cnt;
             }
