@@ -1054,34 +1054,9 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
             const float lse = l != 0.f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
             const float f0 = inv * w0, f1 = inv * w1;
             tc_fence_after_sync();
-            auto read32 = [&](int c, uint32_t (&orr)[32]) {
-                if (used) {
-                    tmem_ld32(tO + c, orr);
-                    tmem_wait_ld(orr);
-#pragma unroll
-                    for (int q = 0; q < 32; ++q)
-                        orr[q] = __float_as_uint(__uint_as_float(orr[q]) * f0);
-                    if (joins) {
-                        uint32_t o1[32];
-                        tmem_ld32(tO1 + c, o1);
-                        tmem_wait_ld(o1);
-#pragma unroll
-                        for (int q = 0; q < 32; ++q)
-                            orr[q] = __float_as_uint(
-                                fmaf(__uint_as_float(o1[q]), f1, __uint_as_float(orr[q])));
-                    }
-                    // a row that saw no key is 0 whatever its accumulator holds
-                    if (l == 0.f) {
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) orr[q] = 0;
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 32; ++q) orr[q] = 0;
-                }
-            };
+            uint16_t* dst[4];
+            float* part = nullptr;
             if (slot < 0) {
-                uint16_t* dst[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int rr = quarter * 32 + i * 8 + (lane >> 2);
@@ -1090,35 +1065,55 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
                         (size_t)(tok0 + tile_tok + tk) * p.Hq + hk * p.G + (rr - tk * p.G);
                     dst[i] = rr < rows && dcheck(row < (size_t)p.T * p.Hq) ? p.o + row * D : nullptr;
                 }
+                const size_t row = (size_t)(tok0 + tile_tok + my_tok) * p.Hq + hk * p.G + my_head;
+                if (row_valid && dcheck(row < (size_t)p.T * p.Hq)) p.lse[row] = lse;
+            } else {
+                const size_t row = (size_t)slot * 256 + (wide ? t * 128 : 0) + r;
+                if (row_valid && dcheck(row < (size_t)512 * kPagedMaxCtas)) {
+                    part = p.part_o + row * D;
+                    p.part_lse[row] = lse;
+                }
+            }
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t orr[32], w[16];
-                    read32(c, orr);
+            for (int c = 0; c < D; c += 32) {
+                uint32_t orr[32];
+                if (used) {
+                    tmem_ld32(tO + c, orr);
+                    tmem_wait_ld(orr);
+#pragma unroll
+                    for (int q = 0; q < 32; ++q)
+                        orr[q] = __float_as_uint(__uint_as_float(orr[q]) * f0);
+                }
+                if (joins) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t o1[16];
+                        tmem_ld16(tO1 + c + 16 * h, o1);
+                        tmem_wait_ld16(o1);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            orr[16 * h + q] = __float_as_uint(
+                                fmaf(__uint_as_float(o1[q]), f1, __uint_as_float(orr[16 * h + q])));
+                    }
+                }
+                // a row that saw no key is 0 whatever its accumulator holds
+                if (!used || l == 0.f) {
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) orr[q] = 0;
+                }
+                if (slot < 0) {
+                    uint32_t w[16];
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         w[q] = pack_bf16x2(__uint_as_float(orr[2 * q]),
                                            __uint_as_float(orr[2 * q + 1]));
                     paged_store_chunk<D>(stage, w, lane, dst, c);
-                }
-                if (row_valid) {
-                    const size_t row = (size_t)(tok0 + tile_tok + my_tok) * p.Hq + hk * p.G + my_head;
-                    if (dcheck(row < (size_t)p.T * p.Hq)) p.lse[row] = lse;
-                }
-            } else {
-                const size_t row = (size_t)slot * 256 + (wide ? t * 128 : 0) + r;
-                float* dst = p.part_o + row * D;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t orr[32];
-                    read32(c, orr);
-                    if (row_valid && dcheck(row < (size_t)512 * kPagedMaxCtas)) {
+                } else if (part) {
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            *reinterpret_cast<uint4*>(dst + c + 4 * q) = make_uint4(
-                                orr[4 * q], orr[4 * q + 1], orr[4 * q + 2], orr[4 * q + 3]);
-                    }
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<uint4*>(part + c + 4 * q) = make_uint4(
+                            orr[4 * q], orr[4 * q + 1], orr[4 * q + 2], orr[4 * q + 3]);
                 }
-                if (row_valid && dcheck(row < (size_t)512 * kPagedMaxCtas)) p.part_lse[row] = lse;
             }
         }
         if (writes) {
@@ -1240,6 +1235,18 @@ __global__ void __launch_bounds__(kPagedMergeThreads)
     const int c = blockIdx.x;
     const PagedPiece first = p.pieces[2 * c + 1];
     if (!first.valid) return;
+    // how many pieces the unit has: up to the one marked last
+    int pieces = 1;
+    for (const int lane = threadIdx.x & 31;; pieces += 32) {
+        const int at = c + pieces + lane;
+        const bool end = at >= ctas || !p.pieces[2 * at].valid || p.pieces[2 * at].last;
+        const unsigned m = __ballot_sync(0xffffffffu, end);
+        if (m) {
+            const int i = __ffs(m) - 1, last = c + pieces + i;
+            pieces += i + (last < ctas && p.pieces[2 * last].valid ? 1 : 0);
+            break;
+        }
+    }
     constexpr float kLog2e = 1.4426950408889634f;
     const int col = threadIdx.x % kPerRow;
     // R: row of the unit's (at most) 256
@@ -1248,28 +1255,34 @@ __global__ void __launch_bounds__(kPagedMergeThreads)
         if (r >= min(max(first.ntok - t * p.tpt, 0), p.tpt) * p.G) continue;
         float M = -INFINITY, W = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        int slot = 2 * c + 1;
-        for (;;) {
-            const size_t row = (size_t)slot * 256 + R;
-            const float ls = p.part_lse[row];
-            const float4 x = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * col);
-            const int last = p.pieces[slot].last;
-            const float mn = fmaxf(M, ls);
-            if (mn != -INFINITY) {
-                // NaN partials stay NaN: fmaxf drops them from the maximum, not from W
-                const float a = fast_exp2((M - mn) * kLog2e), w = fast_exp2((ls - mn) * kLog2e);
-                W = W * a + w;
-                acc.x = acc.x * a + w * x.x;
-                acc.y = acc.y * a + w * x.y;
-                acc.z = acc.z * a + w * x.z;
-                acc.w = acc.w * a + w * x.w;
-                M = mn;
-            } else if (!(ls == -INFINITY)) {
-                W = ls;   // NaN and nothing before it
+        // piece 0 is in slot 2 c + 1, piece i > 0 in slot 2 (c + i); four in flight
+        for (int i0 = 0; i0 < pieces; i0 += 4) {
+            float ls[4];
+            float4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = min(i0 + k, pieces - 1);
+                const size_t row = (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * 256 + R;
+                ls[k] = p.part_lse[row];
+                x[k] = *reinterpret_cast<const float4*>(p.part_o + row * D + 4 * col);
             }
-            if (last) break;
-            slot = (slot | 1) + 1;   // the next CTA's continuing piece
-            if (slot >= 2 * ctas || !p.pieces[slot].valid) break;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (i0 + k >= pieces) break;
+                const float mn = fmaxf(M, ls[k]);
+                if (mn != -INFINITY) {
+                    // NaN partials stay NaN: fmaxf drops them from the maximum, not from W
+                    const float a = fast_exp2((M - mn) * kLog2e), w = fast_exp2((ls[k] - mn) * kLog2e);
+                    W = W * a + w;
+                    acc.x = acc.x * a + w * x[k].x;
+                    acc.y = acc.y * a + w * x[k].y;
+                    acc.z = acc.z * a + w * x[k].z;
+                    acc.w = acc.w * a + w * x[k].w;
+                    M = mn;
+                } else if (!(ls[k] == -INFINITY)) {
+                    W = ls[k];   // NaN and nothing before it
+                }
+            }
         }
         const int tk = r / p.G;
         const size_t row =
