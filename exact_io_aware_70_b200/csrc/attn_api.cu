@@ -718,19 +718,26 @@ attn_status_t launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const C
         sms = di.sms;
     }
     const int grid = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
-    kern<<<grid, T::kThreads, T::kSmemBytes, stream>>>(tq, tk, tv, p);
-    // the merge's launch overlaps the attention kernel (it waits for that one's end itself)
-    constexpr int kUnitRows = N ? N : 256;
-    constexpr int kBlocks = kUnitRows * D / 4 / kPagedMergeThreads;   // one pass over the rows
+    // both launches overlap what runs before them: each kernel waits for its end itself
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, kBlocks < 8 ? kBlocks : 8);
-    cfg.blockDim = dim3(kPagedMergeThreads);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(T::kThreads);
+    cfg.dynamicSmemBytes = T::kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
+    constexpr int kUnitRows = N ? N : 256;
+    constexpr int kBlocks = kUnitRows * D / 4 / kPagedMergeThreads;   // one pass over the rows
+    cfg.gridDim = dim3(grid, kBlocks < 8 ? kBlocks : 8);
+    cfg.blockDim = dim3(kPagedMergeThreads);
+    cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, attn_paged_merge_kernel<D>, p, grid) != cudaSuccess) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;

@@ -1189,6 +1189,8 @@ __global__ void __launch_bounds__(PagedTraits<D>::kThreads, 1)
         tmem_relinquish();
     }
     // the staging area is free until the first epilogue
+    // nothing that an earlier kernel may still write or read was touched so far
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const PagedStretch st =
         paged_schedule<T::kThreads>(p, reinterpret_cast<long long*>(smem + T::kOffStage));
     tc_fence_before_sync();

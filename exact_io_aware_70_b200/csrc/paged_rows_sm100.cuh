@@ -495,6 +495,8 @@ __global__ void __launch_bounds__(PagedTraits<D, N>::kThreads, 1)
         reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     fence_async_shared();
     // P's area is free until the first tile
+    // nothing that an earlier kernel may still write or read was touched so far
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const PagedStretch st =
         paged_schedule<T::kThreads>(p, reinterpret_cast<long long*>(smem + T::kOffStage));
     tc_fence_before_sync();
