@@ -906,29 +906,27 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
     volatile float2* ml = reinterpret_cast<volatile float2*>(sh.smem + T::kOffMl);
     const uint32_t masks = smem_addr(sh.smem) + T::kOffMask;
     const uint32_t stage = smem_addr(sh.smem) + T::kOffStage + warp * T::kStageWarpBytes;
-    const int my_tok = r / p.G, my_head = r - my_tok * p.G;
     const float c2 = p.scale_log2;
     uint32_t it = 0, s_cnt = 0, ml_cnt = 0;
-    uint32_t o_used[2] = {0, 0};
+    uint32_t o_par = 0;                      // uses of O by group 0 (bit 0) and 1 (bit 1), mod 2
 
+    // A unit's record is kept (not released) until its end, and read where it is needed: with a
+    // row of scores in registers there is no room for its fields.
     for (uint32_t units = 0;; ++units) {
         const int ri = units % T::kUnits;
         if (!paged_warp_wait<false>(b.unit_full(ri), (units / T::kUnits) & 1, abort_flag)) return;
         const volatile PagedUnit& uu = ring[ri];
-        const int kind = uu.kind, hk = uu.hk, tok0 = uu.tok, ntok = uu.ntok, pos0 = uu.pos0;
-        const int len = uu.len, key0 = uu.key0, un[2] = {uu.n0, uu.n1}, slot = uu.slot;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b.unit_empty(ri));
-        if (kind == 0) break;
-        const bool wide = kind == 2;
-        const int n = un[t];
-        const int tile_tok = wide ? t * p.tpt : 0;          // first token of this Q tile
-        // rows [0, rows) of the tile have a token
-        const int rows = min(max(ntok - tile_tok, 0), p.tpt) * p.G;
-        const bool active = quarter * 32 < rows;            // any of this warp's rows
-        // keys [0, lim) of the sequence are visible to this row
-        const int lim = (p.causal && len != 0x7fffffff) ? min(len, pos0 + tile_tok + my_tok + 1)
-                                                        : len;
+        if (uu.kind == 0) break;
+        const bool wide = uu.kind == 2;
+        const int n = t ? uu.n1 : uu.n0;
+        // rows [0, rows_of()) of the tile have a token; token_of(): the tile's first one
+        auto token_of = [&]() { return wide ? t * p.tpt : 0; };
+        auto rows_of = [&]() { return min(max(uu.ntok - token_of(), 0), p.tpt) * p.G; };
+        const bool active = quarter * 32 < rows_of();       // any of this warp's rows
+        // keys [0, lim) of the piece's are visible to this row
+        int lim = uu.len;
+        if (p.causal && lim != 0x7fffffff) lim = min(lim, uu.pos0 + token_of() + r / p.G + 1);
+        lim -= uu.key0;
         float m_ref = -INFINITY, l = 0.f;
 
         for (int i = 0; i < n; ++i) {
@@ -944,14 +942,20 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
             // before this tile's P V has freed V's slot
             const uint32_t x = it + k;
             if (!paged_warp_wait<false>(b.mask_full(x % T::kMasks), (x / T::kMasks) & 1, abort_flag)) return;
-            const uint4 mask = ld_shared_v4(masks + 16 * (x % T::kMasks));
+            const uint32_t mask_at = masks + 16 * (x % T::kMasks);
+            bool masked;
+            {
+                const uint4 mask = ld_shared_v4(mask_at);
+                masked = lim - k * 128 < 128 || (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu;
+            }
             tc_fence_after_sync();
             uint32_t sr[128];
             tmem_ld128(tS, sr);
             tmem_wait_ld128(sr);
-            const int cl = (int)max(-1ll, min(128ll, (long long)lim - key0 - (long long)k * 128));
-            if (cl < 128 || (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu) {
+            if (masked) {
                 // keys that exist and lie before the row's limit
+                const int cl = lim - k * 128;
+                const uint4 mask = ld_shared_v4(mask_at);
                 const uint32_t seen[4] = {mask.x & low_bits(cl), mask.y & low_bits(cl - 32),
                                           mask.z & low_bits(cl - 64), mask.w & low_bits(cl - 96)};
 #pragma unroll
@@ -1017,12 +1021,13 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
             f2_unpack(lsum_b, lb0, lb1);
             l = l * alpha + ((la0 + la1) + (lb0 + lb1));
         }
-        it += wide ? max(un[0], un[1]) : un[0] + un[1];
+        const int n0 = uu.n0, n1 = uu.n1;
+        it += wide ? max(n0, n1) : n0 + n1;
 
         // ---- epilogue
-        const bool joins = !wide && un[1] > 0;   // group 0 joins both groups' results
+        const bool joins = !wide && n1 > 0;      // group 0 joins both groups' results
         const bool used = n > 0;
-        if (used && !paged_warp_wait<false>(b.o_final(t), o_used[t] & 1, abort_flag)) return;
+        if (used && !paged_warp_wait<false>(b.o_final(t), (o_par >> t) & 1, abort_flag)) return;
         float w0 = 1.f, w1 = 0.f;
         if (joins) {
             if (t == 1) {
@@ -1033,7 +1038,7 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
             } else {
                 // group 1 has waited for its own o_final by then
                 if (!paged_warp_wait<false>(b.ml_full(0), ml_cnt & 1, abort_flag)) return;
-                if (!paged_warp_wait<false>(b.o_final(1), o_used[1] & 1, abort_flag)) return;
+                if (!paged_warp_wait<false>(b.o_final(1), o_par >> 1, abort_flag)) return;
                 const float m1 = ml[r].x, l1 = ml[r].y;
                 const float m = fmaxf(m_ref, m1);
                 const float mb = m == -INFINITY ? 0.f : m;
@@ -1045,10 +1050,11 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
             }
             ++ml_cnt;
         }
-        for (int x = 0; x < 2; ++x)
-            if (un[x] > 0) ++o_used[x];
+        o_par ^= (n0 > 0 ? 1u : 0u) | (n1 > 0 ? 2u : 0u);
         const bool writes = wide || t == 0;      // group 1 of a narrow unit only feeds group 0
         if (writes && active) {
+            const int rows = rows_of(), tile_tok = token_of(), slot = uu.slot, hk = uu.hk, tok0 = uu.tok;
+            const int my_tok = r / p.G, my_head = r - my_tok * p.G;
             const bool row_valid = r < rows;
             const float inv = l != 0.f ? 1.0f / l : 0.f;
             const float lse = l != 0.f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
@@ -1120,6 +1126,8 @@ __device__ void paged_softmax(const PagedParams& p, uint32_t tbase,
             if (used) softmax_arrive<true>(b.o_free(t), lane);
             if (joins) softmax_arrive<true>(b.o_free(1), lane);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.unit_empty(ri));
     }
 }
 
