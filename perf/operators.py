@@ -205,7 +205,8 @@ def prepare(c, seed):
             s.k, s.v = randn(s.T, Hkv, d), randn(s.T, Hkv, d)
         t, b, i = _rows(s)
         pos = s.ctx_lens[b].long() + i
-        slot = s.table[b, pos // ps].long() * ps + pos % ps
+        # (a padding row's place can lie past the table: it gets no slot)
+        slot = s.table[b, (pos // ps).clamp(max=s.max_pages - 1)].long() * ps + pos % ps
         s.slots = torch.where(t < s.cu[-1], slot, -1)
         return s
 
