@@ -981,7 +981,7 @@ bool launch_topk(const SelectParams& p, cudaStream_t st) {
 
 template <int D, int ROWS>
 bool launch_score(const SelectParams& p, cudaStream_t st) {
-    constexpr int kSmem = (ROWS + kScorePages) * 4 * D;
+    constexpr int kSmem = kScoreABytes<D, ROWS> + kScorePages * 4 * D;
     const int dev = current_device();
     if (dev < 0 || dev >= 64) return false;
     {

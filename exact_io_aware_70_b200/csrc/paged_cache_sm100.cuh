@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
 //      the few between are scored again in fp64 (where the sum of a row's exact products
 //      is all but exact) and the best of them fill up the choice.
 // Scoring every page in fp64 ran 287 us on 1053 rows x 8 heads x 246 pages (1.06e9
-// terms for 32 query heads); this SELECT_US us.
+// terms for 32 query heads); this way the choice takes 62.
 struct SelectParams {
     const uint16_t* q;          // bf16 [T, Hq, D], q_stride elements from row to row
     const uint16_t* bounds;     // bf16 [num_pages, Hkv, 2, D]
@@ -450,12 +450,16 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 // rows), so the products are left to mma.sync, which needs no set-up.
 constexpr int kScoreThreads = 128, kScorePages = 64;
 
+// Bytes of the first operand, or of the scores that take its place (at D = 64 they are larger).
+template <int D, int ROWS>
+constexpr int kScoreABytes = (ROWS * (4 * D > 65 * 4 ? 4 * D : 65 * 4) + 127) / 128 * 128;
+
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const SelectParams p) {
     constexpr int kTerms = 2 * D, kRowBytes = 2 * kTerms, kChunks = kRowBytes / 16;
     extern __shared__ __align__(128) uint8_t s_tiles[];
     uint8_t* sA = s_tiles;                                // [ROWS][2 D] bf16, 16-byte chunks swizzled
-    uint8_t* sB = s_tiles + ROWS * kRowBytes;             // [64 pages][2 D]
+    uint8_t* sB = s_tiles + kScoreABytes<D, ROWS>;        // [64 pages][2 D]
     float* sS = reinterpret_cast<float*>(s_tiles);        // [ROWS][65] scores, over A when it is done
     __shared__ float s_sum[ROWS], s_red[kScoreThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

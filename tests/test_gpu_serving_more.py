@@ -206,6 +206,25 @@ def test_nan_keys_stay_within_their_rows():
         assert (sel[:new[0], 1] == 3).any(-1).all()
 
 
+@pytest.mark.parametrize("new,ctx,Hq,Hkv,d,ps,K,first,last", [
+    ([40, 30], [900, 2000], 8, 1, 64, 16, 20, 0, 2), ([19, 15, 19], [4255, 1918, 2622], 8, 1, 64, 128, 15, 0, 2),
+    ([70], [1100], 32, 1, 64, 16, 30, 0, 0), ([3] * 30, [200] * 30, 4, 4, 128, 16, 5, 1, 1),
+    ([150], [20], 5, 5, 64, 16, 6, 0, 1), ([65, 1, 64], [700, 30, 0], 16, 1, 128, 32, 9, 0, 1),
+    ([9], [5000], 33, 1, 64, 16, 60, 2, 2), ([2, 2, 2], [600, 700, 1100], 64, 1, 64, 16, 11, 0, 0),
+])
+def test_select_of_many_rows(new, ctx, Hq, Hkv, d, ps, K, first, last):
+    """Several rounds of rows against one tile of pages, several sequences in a tile of rows."""
+    m = gpu_util.ea()
+    s = _upload(pu.make_step(new, ctx, Hq, Hkv, d, ps, seed=K, pad=1, poison=False))
+    kb = pu.page_bounds(s.kc)
+    sel = torch.full((s.T, Hkv, K), -7, dtype=torch.int32, device="cuda")
+    ws = torch.empty(m.attn_page_select_workspace_bytes(s.T, Hkv, s.max_pages), dtype=torch.uint8,
+                     device="cuda")
+    m.attn_page_select(s.dq, kb.cuda(), s.dtable, s.dcu, s.dseq, sel, ps, first, last, ws)
+    assert m.attn_status() == 0
+    assert torch.equal(sel.cpu(), pu.ref_select(s, kb, K, first, last))
+
+
 def test_long_batches_of_sequences():
     """More sequences than a CTA has threads."""
     new = [1 if i % 3 else 0 for i in range(1300)]
