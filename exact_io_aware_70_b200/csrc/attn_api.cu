@@ -818,8 +818,6 @@ attn_status_t paged_entry(const void* q, const void* k_cache, const void* v_cach
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     p.causal = causal;
-    p.unit_cost = 128;
-    p.min_stretch = 512;
     p.scale_log2 = scale * kLog2e;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (d == 128)

@@ -20,10 +20,15 @@
 //     key tiles of the same Q tile, and group 0 joins the two results, reading
 //     both accumulators from tensor memory.
 //   * All units are laid on one line, each as long as the keys it sees (plus a
-//     constant for its start), and every CTA gets an equal stretch of it. Units that a stretch's end cuts leave
-//     fp32 partial rows in the workspace (at most two pieces per CTA); a
-//     second kernel joins them. The cut needs only the lengths, which every
-//     CTA scans itself: the host never learns them and no plan is kept.
+//     constant for its start), and every CTA gets an equal stretch of it. Units
+//     that a stretch's end cuts leave fp32 partial rows in the workspace (at
+//     most two pieces per CTA); a second kernel joins them. The cut needs only
+//     the lengths, which every CTA scans itself: the host never learns them and
+//     no plan is kept.
+//   * Warps 0-3 and 4-7 are the softmax groups of Q tile 0 and 1 (one thread per
+//     row), warp 8 loads tiles by TMA, one thread of warp 9 issues the products
+//     (S_t = Q_t K^T, then O_t += P_t V with P_t over S_t in tensor memory),
+//     warp 10 cleans V tiles (below), warp 11 plans units ahead.
 //   * Key tiles are 128 keys: 128 / page_size boxes of a tensor map over the
 //     cache, one lane of the producer warp per box. A page-table entry out of
 //     range, and everything past the last key, is read from a coordinate
@@ -31,6 +36,13 @@
 //     softmax which keys exist. What a page still holds behind the sequence's
 //     last token may be anything (NaN too): its scores are replaced, and its V
 //     rows are zeroed in shared memory by a warp of their own before P V.
+//
+// Few rows per sequence go to paged_rows_sm100.cuh instead. Measured (CUDA graph, 2 sequences of
+// 2048 and 1021 new tokens behind 14K and 7K keys, 32 query heads on 8, d = 128): 700 us, 1000
+// TFLOP/s of the visible pairs. What bounds it is the issuing thread, as in the dense
+// forward (a product costs it about 0.48 us of queueing for 0.27 us of tensor time), and on short
+// prompts (8 of up to 1024 tokens, 12 heads of 64: 53 us) the start of units and
+// the instruction fetch of code that runs a few times only.
 #pragma once
 
 #include <cstdint>
@@ -43,6 +55,12 @@
 namespace eattn {
 
 constexpr int kPagedMaxCtas = 160;     // slots of the workspace; the grid is at most this
+// In keys: what starting a unit costs; the least stretch worth a CTA of its own; and how near a
+// cut may come to a unit's end before it is moved there (a piece costs its CTA a Q load and
+// an epilogue, and the merge a pass). Measured: 128 to 640, 256 to 1024 within 2% of each other on
+// decode, drafts, chunks and prompts; moved cuts (0 -> 128) 58.9 -> 55.6 us on prompts of up to
+// 1024 tokens, 300 and more 4% slower on drafts.
+constexpr int kPagedUnitCost = 128, kPagedMinStretch = 512, kPagedSnap = 128;
 constexpr int kPagedListMax = 480;     // entries of a sparse row's list of key runs
 
 // One CTA's partial rows of a unit that its stretch covers only in part.
@@ -68,8 +86,6 @@ struct PagedParams {
     int tpt, unit_tok;        // tokens of a Q tile and of a unit
     int page_shift, max_pages, num_pages;
     int causal;
-    // in keys: what starting a unit costs, and the least stretch worth a CTA of its own
-    int unit_cost, min_stretch;
     float scale_log2;
 };
 
@@ -230,7 +246,7 @@ struct PagedLine {
         n = s.n;
         m = (s.n + U - 1) / U;
         slope = (!p.sel && p.causal) ? 1 : 0;
-        base = p.unit_cost +
+        base = kPagedUnitCost +
                (p.sel ? ((long long)p.K << p.page_shift) : p.causal ? max(s.len - s.n, 0) : s.len);
     }
     __device__ __forceinline__ long long unit(int q) const {
@@ -280,12 +296,12 @@ __device__ __forceinline__ PagedStretch paged_schedule(const PagedParams& p, lon
     for (int w = 0; w < kWarps; ++w) total += red[w];
     __syncthreads();
     long long chunk = div_fast(total + gridDim.x - 1, gridDim.x);
-    if (chunk < p.min_stretch) chunk = p.min_stretch;
+    if (chunk < kPagedMinStretch) chunk = kPagedMinStretch;
     PagedStretch st;
     st.block = 1;
     if (p.sel) {   // about as many tokens as one stretch holds for all K/V heads
         const long long all_heads =
-            (p.unit_cost + ((long long)p.K << p.page_shift)) * p.Hkv;
+            (kPagedUnitCost + ((long long)p.K << p.page_shift)) * p.Hkv;
         st.block = (int)min(max(div_fast(chunk + all_heads / 2, all_heads), 1ll), 1ll << 20);
     }
     const long long start = chunk * blockIdx.x;
@@ -393,6 +409,19 @@ struct PagedWalk {
             }
             rem -= line.begin(q);
         }
+        // (the CTA before moves its end by the same rule)
+        const long long ulen = line.unit(q);
+        if (rem > 0 && rem < kPagedSnap) {
+            left += rem;
+            rem = 0;
+        } else if (rem > 0 && ulen - rem < kPagedSnap) {
+            advance(p, ulen - rem);
+        }
+    }
+    // how far into its unit the stretch goes (0: it ends before)
+    __device__ __forceinline__ long long end(const PagedParams& p, long long ulen) const {
+        const long long e = rem + left;
+        return e >= ulen ? ulen : e < kPagedSnap ? 0 : ulen - e < kPagedSnap ? ulen : e;
     }
     // past the part of unit q that [rem, rem + taken) is
     __device__ __forceinline__ void advance(const PagedParams& p, long long taken) {
@@ -439,7 +468,7 @@ __device__ void paged_planner(const PagedParams& p, const PagedStretch& st, cons
         const int ri = units % T::kUnits;
         PagedUnit u;
         u.kind = 0;
-        const bool more = w.left > 0;
+        const bool more = w.left > 0 && w.end(p, w.line.unit(w.q)) > 0;
         // sparse: the row's first 32 entries and their pages, read while the ring is full
         int ahead_e = -1, ahead_page = -1;
         auto visible = [&](int e) {   // (and so in the table)
@@ -455,7 +484,7 @@ __device__ void paged_planner(const PagedParams& p, const PagedStretch& st, cons
             return;
         if (more) {
             const long long ulen = w.line.unit(w.q);
-            const long long p0 = w.rem, p1 = min(ulen, w.rem + w.left);
+            const long long p0 = w.rem, p1 = w.end(p, ulen);
             u.seq = w.sb;
             u.keys = u.len = w.s.len;
             u.hk = w.hk;
@@ -520,7 +549,7 @@ __device__ void paged_planner(const PagedParams& p, const PagedStretch& st, cons
             }
             const int all = max(tiles[0], tiles[1]);
             auto tile_at = [&](long long pos) -> int {
-                const long long k = (pos - p.unit_cost) >> 7;
+                const long long k = (pos - kPagedUnitCost) >> 7;
                 return k < 0 ? 0 : k > all ? all : (int)k;
             };
             const int k0 = p0 == 0 ? 0 : tile_at(p0);
