@@ -38,10 +38,10 @@
 //     rows are zeroed in shared memory by a warp of their own before P V.
 //
 // Few rows per sequence go to paged_rows_sm100.cuh instead. Measured (CUDA graph, 2 sequences of
-// 2048 and 1021 new tokens behind 14K and 7K keys, 32 query heads on 8, d = 128): 700 us, 1000
-// TFLOP/s of the visible pairs. What bounds it is the issuing thread, as in the dense
+// 2048 and 957 new tokens behind 14.3K and 11.3K keys, 32 query heads on 8, d = 128): 700 us,
+// 1000 TFLOP/s of the visible pairs. What bounds it is the issuing thread, as in the dense
 // forward (a product costs it about 0.48 us of queueing for 0.27 us of tensor time), and on short
-// prompts (8 of up to 1024 tokens, 12 heads of 64: 53 us) the start of units and
+// prompts (8 of up to 1024 tokens, 12 heads of 64: 55 us) the start of units and
 // the instruction fetch of code that runs a few times only.
 #pragma once
 

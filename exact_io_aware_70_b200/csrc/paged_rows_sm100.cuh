@@ -20,6 +20,13 @@
 // The two softmax groups take alternate key tiles, each with its own issuing
 // thread, so neither waits for the other; they take turns at joining their results
 // (group 0 when it alone had a tile).
+//
+// Warps: 0-3 and 4-7 softmax, 8 loads Q and K, 13 V, 9 and 11 issue the products of
+// group 0 and 1, 10 cleans V tiles, 12 plans. Measured (CUDA graph): 16 sequences of 32768
+// keys, 32 query heads on 8, 327 us = 6.57 TB/s of K/V, the card's copy rate (128-row form:
+// 354); 1098 rows over 16 pages of 64 each, 553 us = 8.3 TB/s, mostly out of L2, bound by the
+// loads' latency with three tile pairs in flight and by units that are 8 tiles long
+// (1449); 7 sequences of up to 6 drafted tokens, 25 us, most of it start-up.
 #pragma once
 
 #include <cfloat>
