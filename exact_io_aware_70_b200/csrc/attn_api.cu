@@ -994,7 +994,7 @@ bool launch_score(const SelectParams& p, cudaStream_t st) {
         }
     }
     const dim3 grid((unsigned)((long long)p.tiles * ((p.T + p.tile_tok - 1) / p.tile_tok)), p.Hkv);
-    attn_page_score_kernel<D, ROWS><<<grid, kScoreThreads, kSmem, st>>>(p);
+    attn_page_score_kernel<D, ROWS><<<grid, kScoreThreads<ROWS>, kSmem, st>>>(p);
     return true;
 }
 

@@ -448,20 +448,25 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 // group) at a time against 64 pages, 2 D terms: 64 or 40 KB of shared memory at D = 128. What
 // bounds it is the read of q and of the bounds (each tile of pages is read once per ROWS
 // rows), so the products are left to mma.sync, which needs no set-up.
-constexpr int kScoreThreads = 128, kScorePages = 64;
+constexpr int kScorePages = 64;
+// Threads of a block: its time is that of dependent steps (lookup, loads, products, maxima), so
+// 64 rows get eight warps (38 us against 45 with four, at 1,098 tokens, 32 and 8 heads, up to 246 pages a token).
+template <int ROWS>
+constexpr int kScoreThreads = ROWS == 64 ? 256 : 128;
 
 // Bytes of the first operand, or of the scores that take its place (at D = 64 they are larger).
 template <int D, int ROWS>
 constexpr int kScoreABytes = (ROWS * (4 * D > 65 * 4 ? 4 * D : 65 * 4) + 127) / 128 * 128;
 
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(const SelectParams p) {
+    constexpr int kThreads = kScoreThreads<ROWS>;
     constexpr int kTerms = 2 * D, kRowBytes = 2 * kTerms, kChunks = kRowBytes / 16;
     extern __shared__ __align__(128) uint8_t s_tiles[];
     uint8_t* sA = s_tiles;                                // [ROWS][2 D] bf16, 16-byte chunks swizzled
     uint8_t* sB = s_tiles + kScoreABytes<D, ROWS>;        // [64 pages][2 D]
     float* sS = reinterpret_cast<float*>(s_tiles);        // [ROWS][65] scores, over A when it is done
-    __shared__ float s_sum[ROWS], s_red[kScoreThreads / 32];
+    __shared__ float s_sum[ROWS], s_red[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hk = blockIdx.y, tok_tile = blockIdx.x / p.tiles, tile = blockIdx.x - tok_tile * p.tiles;
     const int page0 = tile * kScorePages;
@@ -485,7 +490,8 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
         __syncthreads();          // the last round's reads of shared memory are done
         // ---- bounds of the tile's pages, and the largest sum of squares of one page's
         float top = 0.f;
-        constexpr int kRowsPerPass = kScoreThreads / kChunks, kBatch = 8;
+        constexpr int kRowsPerPass = kThreads / kChunks;
+        constexpr int kBatch = kScorePages / kRowsPerPass < 8 ? kScorePages / kRowsPerPass : 8;
         const int c = tid % kChunks;
         for (int r0 = tid / kChunks; r0 < kScorePages; r0 += kBatch * kRowsPerPass) {
             uint4 x[kBatch];
@@ -531,11 +537,11 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
         float best = -INFINITY;       // G > ROWS: of this thread's page, over the rounds
         for (int r0 = 0; r0 < rows; r0 += ROWS) {
             __syncthreads();          // (the last reads of A, scores and sums)
-            constexpr int kHalf = kChunks / 2, kLoads = ROWS * kHalf / kScoreThreads;
+            constexpr int kHalf = kChunks / 2, kLoads = ROWS * kHalf / kThreads;
             uint4 x[kLoads];       // all in flight before the first is used
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
-                const int row = tid / kHalf + k * (kScoreThreads / kHalf);
+                const int row = tid / kHalf + k * (kThreads / kHalf);
                 x[k] = make_uint4(0, 0, 0, 0);
                 if (r0 + row < rows) {
                     const int tk = (r0 + row) / p.G, h = r0 + row - tk * p.G;
@@ -546,7 +552,7 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
             }
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
-                const int row = tid / kHalf + k * (kScoreThreads / kHalf), c = tid % kHalf;
+                const int row = tid / kHalf + k * (kThreads / kHalf), c = tid % kHalf;
                 const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
                 uint32_t neg[4], pos[4];
                 float sum = 0.f;
@@ -569,9 +575,10 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
                 if (c == 0) s_sum[row] = sum;
             }
             __syncthreads();
-            // ---- warp w: rows 16 w .. against all 64 pages, or 16 rows against pages 16 w ..
-            constexpr int kN = ROWS / 16;             // groups of 16 pages per warp
-            const int wr = ROWS == 64 ? 16 * warp : 0, wp = ROWS == 64 ? 0 : 16 * warp;
+            // ---- warp w: 16 of the rows against 32 pages (ROWS = 64) or 16 pages
+            constexpr int kN = ROWS == 64 ? 2 : 1;    // groups of 16 pages per warp
+            const int wr = ROWS == 64 ? 16 * (warp & 3) : 0;
+            const int wp = ROWS == 64 ? 32 * (warp >> 2) : 16 * warp;
             float acc[2 * kN][4];
 #pragma unroll
             for (int n = 0; n < 2 * kN; ++n)
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
             const int ntok = p.G <= ROWS ? rows / p.G : 1;
             const int heads = min(p.G, rows - r0 < ROWS ? rows - r0 : ROWS);
             const int in = p.G <= ROWS ? p.G : heads;
-            for (int i = tid; i < ntok * kScorePages; i += kScoreThreads) {
+            for (int i = tid; i < ntok * kScorePages; i += kThreads) {
                 const int tk = i / kScorePages, col = i - tk * kScorePages;
                 float m = best;
                 for (int h = 0; h < in; ++h) {
@@ -627,7 +634,7 @@ __global__ void __launch_bounds__(kScoreThreads) attn_page_score_kernel(const Se
                 float sum = 0.f;
                 for (int h = 0; h < in; ++h) sum = fmaxf(sum, s_sum[tid * p.G + h]);
                 float b = s_red[0];
-                for (int w = 1; w < kScoreThreads / 32; ++w) b = fmaxf(b, s_red[w]);
+                for (int w = 1; w < kThreads / 32; ++w) b = fmaxf(b, s_red[w]);
                 float e = sqrtf(sum) * sqrtf(b) * 3.3e-5f;
                 float* dst = p.err + ((size_t)(s0 + tid) * p.Hkv + hk) * p.tiles + tile;
                 if (r0 > 0) e = fmaxf(e, *dst);   // this thread's own, of the first heads
