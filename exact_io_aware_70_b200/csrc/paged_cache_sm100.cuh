@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
 //      the few between are scored again in fp64 (where the sum of a row's exact products
 //      is all but exact) and the best of them fill up the choice.
 // Scoring every page in fp64 ran 287 us on 1098 rows x 8 K/V heads x up to 246 pages
-// (0.8e9 terms for 32 query heads); this way the choice takes 62.
+// (0.8e9 terms for 32 query heads); this way the choice takes 56.
 struct SelectParams {
     const uint16_t* q;          // bf16 [T, Hq, D], q_stride elements from row to row
     const uint16_t* bounds;     // bf16 [num_pages, Hkv, 2, D]
@@ -450,13 +450,20 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 // rows), so the products are left to mma.sync, which needs no set-up.
 constexpr int kScorePages = 64;
 // Threads of a block: its time is that of dependent steps (lookup, loads, products, maxima), so
-// 64 rows get eight warps (38 us against 45 with four, at 1,098 tokens, 32 and 8 heads, up to 246 pages a token).
+// 64 rows get eight warps (38 us against 45 with four, at 1,098 tokens of 32 heads on 8 and up
+// to 246 pages).
 template <int ROWS>
 constexpr int kScoreThreads = ROWS == 64 ? 256 : 128;
 
 // Bytes of the first operand, or of the scores that take its place (at D = 64 they are larger).
 template <int D, int ROWS>
 constexpr int kScoreABytes = (ROWS * (4 * D > 65 * 4 ? 4 * D : 65 * 4) + 127) / 128 * 128;
+
+// Where a sum of squares begins, so that squares too small for 32 bits (and what
+// 2^-126 cuts off elsewhere) do not make a bound of 0 for numbers that are not.
+__device__ __forceinline__ float least_sum(const uint32_t (&w)[4]) {
+    return ((w[0] | w[1] | w[2] | w[3]) & 0x7FFF7FFFu) ? 0x1p-100f : 0.f;
+}
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(const SelectParams p) {
@@ -512,7 +519,7 @@ __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(co
             for (int k = 0; k < kBatch; ++k) {
                 const int row = r0 + k * kRowsPerPass;   // (kScorePages is a multiple of a batch)
                 const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                float sum = 0.f;
+                float sum = least_sum(w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     sum = fmaf(bf16_lo(w[j]), bf16_lo(w[j]), sum);
@@ -555,7 +562,7 @@ __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(co
                 const int row = tid / kHalf + k * (kThreads / kHalf), c = tid % kHalf;
                 const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
                 uint32_t neg[4], pos[4];
-                float sum = 0.f;
+                float sum = least_sum(w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float a = bf16_lo(w[j]), b = bf16_hi(w[j]);
@@ -629,7 +636,8 @@ __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(co
             }
             // ---- the error of these sums: 2 D / 16 <= 16 steps that each add 17 numbers, every one
             // of them cut off below 2^-23 of the largest at worst: under 16 * 17 * 2^-23 < 3.3e-5
-            // times sum |q b| <= |q| |b|
+            // times sum |q b| <= |q| |b|, both at least 2^-50 (least_sum), which covers what products
+            // and sums lose below 2^-126 (2 D * 2^-126 <= 2^-118). 0: all scores are exactly 0
             if (tid < ntok) {
                 float sum = 0.f;
                 for (int h = 0; h < in; ++h) sum = fmaxf(sum, s_sum[tid * p.G + h]);

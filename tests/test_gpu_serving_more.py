@@ -225,6 +225,31 @@ def test_select_of_many_rows(new, ctx, Hq, Hkv, d, ps, K, first, last):
     assert torch.equal(sel.cpu(), pu.ref_select(s, kb, K, first, last))
 
 
+@pytest.mark.parametrize("d,Hq,T", [(64, 1, 1), (128, 4, 1), (128, 1, 40)])
+@pytest.mark.parametrize("small", ["q", "bounds", "both"])
+def test_select_of_very_small_numbers(d, Hq, T, small):
+    """Squares of q or of the bounds that are 0 in 32 bits: the choice is still the exact one. Pages 1
+    and 3 score 1 + 2^-26 and 1 in units of the largest product, which 32-bit sums do not tell apart."""
+    m = gpu_util.ea()
+    s = _upload(pu.make_step([T], [16 * 6], Hq, 1, d, 16, seed=1, poison=False))
+    sq, sb = {"q": (-80, 10), "bounds": (0, -80), "both": (-70, -40)}[small]
+    q = torch.full((T, Hq, d), 2.0 ** sq).bfloat16()
+    kb = torch.zeros((s.num_pages, 1, 2, d))
+    for lp, low in ((1, 0.0), (3, 2.0 ** -26)):
+        kb[s.table[0, lp].long(), 0, :, 0] = 2.0 ** sb
+        kb[s.table[0, lp].long(), 0, :, 1] = 2.0 ** sb * low
+    kb = kb.bfloat16()
+    s.q = q
+    sel = torch.full((T, 1, 1), -7, dtype=torch.int32, device="cuda")
+    ws = torch.empty(m.attn_page_select_workspace_bytes(T, 1, s.max_pages), dtype=torch.uint8,
+                     device="cuda")
+    m.attn_page_select(q.cuda(), kb.cuda(), s.dtable, s.dcu, s.dseq, sel, 16, 0, 0, ws)
+    assert m.attn_status() == 0
+    want = pu.ref_select(s, kb, 1, 0, 0)
+    assert (want == 3).all()
+    assert torch.equal(sel.cpu(), want)
+
+
 def test_long_batches_of_sequences():
     """More sequences than a CTA has threads."""
     new = [1 if i % 3 else 0 for i in range(1300)]
