@@ -451,7 +451,8 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 constexpr int kScorePages = 64;
 // Threads of a block: its time is that of dependent steps (lookup, loads, products, maxima), so
 // 64 rows get eight warps (38 us against 45 with four, at 1,098 tokens of 32 heads on 8 and up
-// to 246 pages).
+// to 246 pages); 16 rows, whose blocks are small, gain nothing by them (29.6 against 30.3 us for
+// the whole choice at 16 tokens and 512 pages).
 template <int ROWS>
 constexpr int kScoreThreads = ROWS == 64 ? 256 : 128;
 
