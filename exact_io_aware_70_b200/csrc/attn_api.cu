@@ -994,14 +994,25 @@ bool launch_score(const SelectParams& p, cudaStream_t st) {
         }
     }
     const dim3 grid((unsigned)((long long)p.tiles * ((p.T + p.tile_tok - 1) / p.tile_tok)), p.Hkv);
-    attn_page_score_kernel<D, ROWS><<<grid, kScoreThreads<ROWS>, kSmem, st>>>(p);
-    return true;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kScoreThreads<ROWS>);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_page_score_kernel<D, ROWS>, p) == cudaSuccess;
 }
 
 template <int D>
 attn_status_t launch_select(const SelectParams& p, cudaStream_t st) {
-    if (!(p.tile_tok * p.G <= 16 ? launch_score<D, 16>(p, st) : launch_score<D, 64>(p, st)))
+    if (!(p.tile_tok * p.G <= 16 ? launch_score<D, 16>(p, st) : launch_score<D, 64>(p, st))) {
+        cudaGetLastError();
         return ATTN_ERR_CUDA;
+    }
     // the fewest threads per row whose registers hold its keys
     const bool ok = p.max_pages <= 32 * 8      ? launch_topk<D, 32, 8>(p, st)
                     // few rows: more threads for each, or the row's own steps set the time

@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(co
     const int hk = blockIdx.y, tok_tile = blockIdx.x / p.tiles, tile = blockIdx.x - tok_tile * p.tiles;
     const int page0 = tile * kScorePages;
     const int t0 = tok_tile * p.tile_tok, t1 = min(t0 + p.tile_tok, p.T);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the choice waits by itself
     auto at = [](int row, int chunk) { return row * kRowBytes + ((chunk ^ (row & 7)) << 4); };
 
@@ -662,16 +663,41 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     constexpr int kGroups = THREADS == 32 ? 4 : 1;       // rows per block
     constexpr int kWarps = THREADS / 32;
     __shared__ int s_cnt[2][kWarps];
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the scores are made
     const int tid = threadIdx.x % THREADS, lane = tid & 31, warp = tid >> 5;
     const long long rowi = (long long)blockIdx.x * kGroups + threadIdx.x / THREADS;
-    if (rowi >= (long long)p.T * p.Hkv) return;
+    // Launched while the scores are made, by blocks that have waited for all before them: offsets,
+    // lengths and tables may be read at once, the scores once those blocks are done.
     const int t = (int)(rowi / p.Hkv), hk = (int)(rowi - (long long)t * p.Hkv);
-    const SelectRow row = select_row(p, t, lane);
+    SelectRow row;
+    row.b = -1;
+    row.pages = 0;
+    if (t < p.T) row = select_row(p, t, lane);
+    const int* table = p.block_table + (size_t)max(row.b, 0) * p.max_pages;
+    // thread i holds pages r * THREADS + i
+    uint32_t keep = 0, open = 0;                         // bit r: always chosen / to be ranked
+    int kept = 0, ranked = 0;
+    bool bad = false;
+#pragma unroll
+    for (int r = 0; r < PER; ++r) {
+        const int lp = r * THREADS + tid;
+        if (lp < row.pages) {
+            const int page = __ldg(table + lp);
+            if (page < 0 || page >= p.num_pages) {
+                bad = true;
+            } else if (lp < p.first || lp >= row.pages - p.last) {
+                keep |= 1u << r;
+                ++kept;
+            } else {
+                open |= 1u << r;
+                ++ranked;
+            }
+        }
+    }
+    if (bad) atomicOr(&g_attn_status, kDevErrBadIndex);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (row.b < 0) return;                               // rows of no sequence stay as they were
     int* out = p.sel + rowi * p.K;
     unsigned long long* exact = p.keys + rowi * p.max_pages;
-    const int* table = p.block_table + (size_t)row.b * p.max_pages;
     int flip = 0;
     auto total = [&](int v) -> int {
         v = __reduce_add_sync(0xffffffffu, v);
@@ -709,29 +735,11 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
         }
         return before;
     };
-    // thread i holds pages r * THREADS + i; key 0: not to be ranked
-    uint32_t key[PER];
-    uint32_t keep = 0;                                   // bit r: always chosen
-    int kept = 0, ranked = 0;
-    bool bad = false;
+    uint32_t key[PER];                                   // 0: not to be ranked
 #pragma unroll
-    for (int r = 0; r < PER; ++r) {
-        const int lp = r * THREADS + tid;
-        key[r] = 0;
-        if (lp < row.pages) {
-            const int page = __ldg(table + lp);
-            if (page < 0 || page >= p.num_pages) {
-                bad = true;
-            } else if (lp < p.first || lp >= row.pages - p.last) {
-                keep |= 1u << r;
-                ++kept;
-            } else {
-                key[r] = order_key(reinterpret_cast<const float*>(exact)[lp]);
-                ++ranked;
-            }
-        }
-    }
-    if (bad) atomicOr(&g_attn_status, kDevErrBadIndex);
+    for (int r = 0; r < PER; ++r)
+        key[r] = (open >> r) & 1
+                     ? order_key(reinterpret_cast<const float*>(exact)[r * THREADS + tid]) : 0;
     const int want = p.K - total(kept);                  // to be chosen by their scores
     ranked = total(ranked);
     float err = 0.f;
@@ -872,17 +880,17 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     for (int r = 0; r * THREADS < row.pages; ++r) {
         bool take = (sure >> r) & 1;
         if (unsure > need) {
-            const bool open = (maybe >> r) & 1;
+            const bool mine = (maybe >> r) & 1;
             int all;
-            const int place = base + rank(open, all);
+            const int place = base + rank(mine, all);
             base += all;
             if (unsure <= 32) {
-                take = take || (open && ((picked >> place) & 1));
+                take = take || (mine && ((picked >> place) & 1));
             } else {
-                const unsigned long long k = open ? exact[place] : 0;
+                const unsigned long long k = mine ? exact[place] : 0;
                 int equal;
-                const int eq = rank(open && k == kth, equal);
-                take = take || (open && (k > kth || (k == kth && eq < ties)));
+                const int eq = rank(mine && k == kth, equal);
+                take = take || (mine && (k > kth || (k == kth && eq < ties)));
                 ties = max(0, ties - equal);
             }
         }
