@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
 //      the few between are scored again in fp64 (where the sum of a row's exact products
 //      is all but exact) and the best of them fill up the choice.
 // Scoring every page in fp64 ran 287 us on 1098 rows x 8 K/V heads x up to 246 pages
-// (0.8e9 terms for 32 query heads); this way the choice takes 56.
+// (0.8e9 terms for 32 query heads); this way the choice takes 54.
 struct SelectParams {
     const uint16_t* q;          // bf16 [T, Hq, D], q_stride elements from row to row
     const uint16_t* bounds;     // bf16 [num_pages, Hkv, 2, D]
@@ -443,9 +443,21 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 16 bytes from global to shared memory, zeros where !valid (src must be readable memory still).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Block (x, hk): pages [64 (x % tiles), + 64) for the tile_tok tokens from (x / tiles) *
 // tile_tok on, one sequence of them after another. ROWS = 64 or 16 rows (token, head of the
-// group) at a time against 64 pages, 2 D terms: 64 or 40 KB of shared memory at D = 128. What
+// group) at a time against 64 pages, 2 D terms: 64 or 40 KB of shared memory at D = 128. The
+// bounds come by asynchronous copies, all of a tile's at once (through registers, eight at a
+// time, the choice for 16 tokens of 512 pages took 28.3 us; so: 24.9). What
 // bounds it is the read of q and of the bounds (each tile of pages is read once per ROWS
 // rows), so the products are left to mma.sync, which needs no set-up.
 constexpr int kScorePages = 64;
@@ -470,6 +482,7 @@ template <int D, int ROWS>
 __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(const SelectParams p) {
     constexpr int kThreads = kScoreThreads<ROWS>;
     constexpr int kTerms = 2 * D, kRowBytes = 2 * kTerms, kChunks = kRowBytes / 16;
+    constexpr int kParts = kThreads / kScorePages;        // threads that look at one page's sum
     extern __shared__ __align__(128) uint8_t s_tiles[];
     uint8_t* sA = s_tiles;                                // [ROWS][2 D] bf16, 16-byte chunks swizzled
     uint8_t* sB = s_tiles + kScoreABytes<D, ROWS>;        // [64 pages][2 D]
@@ -497,47 +510,25 @@ __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(co
             continue;
         }
         __syncthreads();          // the last round's reads of shared memory are done
-        // ---- bounds of the tile's pages, and the largest sum of squares of one page's
-        float top = 0.f;
-        constexpr int kRowsPerPass = kThreads / kChunks;
-        constexpr int kBatch = kScorePages / kRowsPerPass < 8 ? kScorePages / kRowsPerPass : 8;
-        const int c = tid % kChunks;
-        for (int r0 = tid / kChunks; r0 < kScorePages; r0 += kBatch * kRowsPerPass) {
-            uint4 x[kBatch];
-            int page[kBatch];
+        // ---- bounds of the tile's pages, all on their way before the first is waited for
+        {
+            constexpr int kRowsPerPass = kThreads / kChunks, kPasses = kScorePages / kRowsPerPass;
+            const int c = tid % kChunks, r0 = tid / kChunks;
+            int page[kPasses];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
+            for (int k = 0; k < kPasses; ++k) {
                 const int lp = page0 + r0 + k * kRowsPerPass;
-                page[k] = r0 + k * kRowsPerPass < kScorePages && lp < pages
-                              ? __ldg(p.block_table + (size_t)first.b * p.max_pages + lp) : -1;
+                page[k] = lp < pages ? __ldg(p.block_table + (size_t)first.b * p.max_pages + lp) : -1;
             }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                x[k] = page[k] >= 0 && page[k] < p.num_pages
-                           ? __ldg(reinterpret_cast<const uint4*>(
-                                       p.bounds + ((size_t)page[k] * p.Hkv + hk) * kTerms) + c)
-                           : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int row = r0 + k * kRowsPerPass;   // (kScorePages is a multiple of a batch)
-                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                float sum = least_sum(w);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sum = fmaf(bf16_lo(w[j]), bf16_lo(w[j]), sum);
-                    sum = fmaf(bf16_hi(w[j]), bf16_hi(w[j]), sum);
-                }
-#pragma unroll
-                for (int off = 1; off < kChunks; off <<= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                top = fmaxf(top, sum);
-                *reinterpret_cast<uint4*>(sB + at(row, c)) = x[k];
+            for (int k = 0; k < kPasses; ++k) {
+                const bool valid = page[k] >= 0 && page[k] < p.num_pages;
+                const size_t row = (size_t)(valid ? page[k] : 0) * p.Hkv + hk;
+                cp_async16(smem_addr(sB) + at(r0 + k * kRowsPerPass, c), p.bounds + row * kTerms + 8 * c,
+                           valid);
             }
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        if (lane == 0) s_red[warp] = top;
+        bool fresh = true;        // until the first round has waited for them
 
         // ---- its rows, as many tokens at a time as fit ROWS (G > ROWS: one, in rounds)
         const int sub = max(1, ROWS / p.G);
@@ -545,7 +536,6 @@ __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(co
         const int rows = (min(te, s0 + sub) - s0) * p.G;
         float best = -INFINITY;       // G > ROWS: of this thread's page, over the rounds
         for (int r0 = 0; r0 < rows; r0 += ROWS) {
-            __syncthreads();          // (the last reads of A, scores and sums)
             constexpr int kHalf = kChunks / 2, kLoads = ROWS * kHalf / kThreads;
             uint4 x[kLoads];       // all in flight before the first is used
 #pragma unroll
@@ -559,6 +549,7 @@ __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(co
                                      (size_t)(hk * p.G + h) * D) + tid % kHalf);
                 }
             }
+            __syncthreads();          // (the last reads of A, scores and sums)
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
                 const int row = tid / kHalf + k * (kThreads / kHalf), c = tid % kHalf;
@@ -583,7 +574,31 @@ __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(co
                     sum += __shfl_xor_sync(0xffffffffu, sum, off);
                 if (c == 0) s_sum[row] = sum;
             }
+            if (fresh) cp_async_wait_all();
             __syncthreads();
+            if (fresh) {
+                // largest sum of squares of a page's terms [part, part + 1) * kTerms / kParts, a part
+                // and 32 pages per warp: the sum of the parts' largest bounds every page's
+                constexpr int kPart = kChunks / kParts;
+                const int row = tid % kScorePages, c0 = tid / kScorePages * kPart;
+                float sum = 0.f;
+#pragma unroll 4
+                for (int k = 0; k < kPart; ++k) {
+                    const uint4 b = *reinterpret_cast<const uint4*>(sB + at(row, c0 + k));
+                    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+                    sum += least_sum(w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sum = fmaf(bf16_lo(w[j]), bf16_lo(w[j]), sum);
+                        sum = fmaf(bf16_hi(w[j]), bf16_hi(w[j]), sum);
+                    }
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1)
+                    sum = fmaxf(sum, __shfl_xor_sync(0xffffffffu, sum, off));
+                if (lane == 0) s_red[warp] = sum;
+                fresh = false;
+            }
             // ---- warp w: 16 of the rows against 32 pages (ROWS = 64) or 16 pages
             constexpr int kN = ROWS == 64 ? 2 : 1;    // groups of 16 pages per warp
             const int wr = ROWS == 64 ? 16 * (warp & 3) : 0;
@@ -643,8 +658,8 @@ __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(co
             if (tid < ntok) {
                 float sum = 0.f;
                 for (int h = 0; h < in; ++h) sum = fmaxf(sum, s_sum[tid * p.G + h]);
-                float b = s_red[0];
-                for (int w = 1; w < kThreads / 32; ++w) b = fmaxf(b, s_red[w]);
+                float b = 0.f;
+                for (int w = 0; w < kParts; ++w) b += fmaxf(s_red[2 * w], s_red[2 * w + 1]);
                 float e = sqrtf(sum) * sqrtf(b) * 3.3e-5f;
                 float* dst = p.err + ((size_t)(s0 + tid) * p.Hkv + hk) * p.tiles + tile;
                 if (r0 > 0) e = fmaxf(e, *dst);   // this thread's own, of the first heads
