@@ -457,7 +457,7 @@ __device__ __forceinline__ void cp_async_wait_all() {
 // tile_tok on, one sequence of them after another. ROWS = 64 or 16 rows (token, head of the
 // group) at a time against 64 pages, 2 D terms: 64 or 40 KB of shared memory at D = 128. The
 // bounds come by asynchronous copies, all of a tile's at once (through registers, eight at a
-// time, the choice for 16 tokens of 512 pages took 28.3 us; so: 24.9). What
+// time, the choice for 16 tokens of 512 pages took 3.4 us longer). What
 // bounds it is the read of q and of the bounds (each tile of pages is read once per ROWS
 // rows), so the products are left to mma.sync, which needs no set-up.
 constexpr int kScorePages = 64;
@@ -677,6 +677,9 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
     attn_page_topk_kernel(const SelectParams p) {
     constexpr int kGroups = THREADS == 32 ? 4 : 1;       // rows per block
     constexpr int kWarps = THREADS / 32;
+    // heads whose exact scores are taken together: with few rows their latency sets the time (16
+    // tokens of 512 pages: 24.9 us one by one, 24.0 so), with many the registers do
+    constexpr int kHeads = THREADS == 128 ? 4 : 1;
     __shared__ int s_cnt[2][kWarps];
     const int tid = threadIdx.x % THREADS, lane = tid & 31, warp = tid >> 5;
     const long long rowi = (long long)blockIdx.x * kGroups + threadIdx.x / THREADS;
@@ -841,23 +844,44 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
                 m &= m - 1;
                 const int lp = r * THREADS + warp * 32 + src;
                 const uint16_t* bnd = p.bounds + ((size_t)__ldg(table + lp) * p.Hkv + hk) * 2 * D;
+                float lo[D / 32], hi[D / 32];
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    lo[c] = __uint_as_float((uint32_t)__ldg(bnd + 32 * c + lane) << 16);
+                    hi[c] = __uint_as_float((uint32_t)__ldg(bnd + D + 32 * c + lane) << 16);
+                }
                 double best = -INFINITY;
                 bool nan = false;
-                for (int g = 0; g < p.G; ++g) {
-                    const uint16_t* q = p.q + (size_t)t * p.q_stride + (size_t)(hk * p.G + g) * D;
-                    double sum = 0;
+                for (int g0 = 0; g0 < p.G; g0 += kHeads) {
+                    float x[kHeads][D / 32];
+                    double sum[kHeads];
 #pragma unroll
-                    for (int c = lane; c < D; c += 32) {
-                        const float x = __uint_as_float((uint32_t)__ldg(q + c) << 16);
-                        const float lo = __uint_as_float((uint32_t)__ldg(bnd + c) << 16);
-                        const float hi = __uint_as_float((uint32_t)__ldg(bnd + D + c) << 16);
-                        sum = fma((double)x, (double)(x >= 0.f ? hi : lo), sum);
+                    for (int g = 0; g < kHeads; ++g) {
+                        // (a head past the last: the last one again)
+                        const uint16_t* q = p.q + (size_t)t * p.q_stride +
+                                            (size_t)(hk * p.G + min(g0 + g, p.G - 1)) * D;
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c)
+                            x[g][c] = __uint_as_float((uint32_t)__ldg(q + 32 * c + lane) << 16);
+                    }
+#pragma unroll
+                    for (int g = 0; g < kHeads; ++g) {
+                        sum[g] = 0;
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c)
+                            sum[g] = fma((double)x[g][c], (double)(x[g][c] >= 0.f ? hi[c] : lo[c]),
+                                         sum[g]);
                     }
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1)
-                        sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                    nan = nan || sum != sum;
-                    best = fmax(best, sum);
+#pragma unroll
+                        for (int g = 0; g < kHeads; ++g)
+                            sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], off);
+#pragma unroll
+                    for (int g = 0; g < kHeads; ++g) {
+                        nan = nan || sum[g] != sum[g];
+                        best = fmax(best, sum[g]);
+                    }
                 }
                 const int place = base + __shfl_sync(0xffffffffu, before, src);
                 if (lane == 0 && dcheck(place < p.max_pages))
