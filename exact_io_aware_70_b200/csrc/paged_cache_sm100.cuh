@@ -781,6 +781,10 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
         }
         least = lowest(least);
         most = ~lowest(~most);
+        // A NaN score has no error bound (the bounds' maxima above leave NaN out), and it may be the
+        // product's alone: 0 times an infinite bound on the side that q's sign does not take. So
+        // with one in the row every page is undecided and the exact scores say what is what.
+        if (most == ~0u) err = INFINITY;
         const int bits = 32 - __clz(least ^ most);
         uint32_t kth = bits == 32 ? 0 : (most >> bits) << bits;
         for (int bit = bits - 1; bit >= 0; --bit) {
