@@ -13,6 +13,25 @@
 
 namespace eattn {
 
+// ----------------------------------------------------- a step's sequences --
+struct PagedSeq {
+    int tok, n, len;   // first row, new tokens, cached keys; all clamped to the tensors
+    bool bad;
+};
+
+// Sequence b of a call with parameters p (offsets, lengths and the sizes that bound them).
+template <class Params>
+__device__ __forceinline__ PagedSeq paged_seq(const Params& p, int b) {
+    PagedSeq s;
+    const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), l = __ldg(p.seq_lens + b);
+    const int cap = p.max_pages << p.page_shift;
+    s.tok = min(max(c0, 0), p.T);
+    s.n = min(max(c1, s.tok), p.T) - s.tok;
+    s.len = min(max(l, 0), cap);
+    s.bad = s.tok != c0 || s.tok + s.n != c1 || s.len != l;
+    return s;
+}
+
 // ---------------------------------------------------------- block tables --
 // Sequence b holds ctx[b] tokens and gets new[b] more. With cu the exclusive
 // prefix sum of new and P that of the pages each one lacks,
@@ -406,8 +425,8 @@ __device__ __forceinline__ SelectRow select_row(const SelectParams& p, int t, in
     if (t < c0 || t >= c1) return r;   // before the first, past the last, or offsets that do not ascend
     const int len = min(max(l, 0), p.max_pages << p.page_shift);
     r.b = lo;
-    r.end = c1;
-    r.pos = len - c1 + t;
+    r.end = min(c1, p.T);          // (as paged_seq clamps it: the positions agree with the attention's)
+    r.pos = len - r.end + t;
     r.pages = r.pos < 0 ? 0 : (r.pos >> p.page_shift) + 1;
     return r;
 }
@@ -711,6 +730,8 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
             }
         }
     }
+    if (blockIdx.x == 0)                                 // lengths and offsets out of range
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) bad = bad || paged_seq(p, b).bad;
     if (bad) atomicOr(&g_attn_status, kDevErrBadIndex);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (row.b < 0) return;                               // rows of no sequence stay as they were

@@ -49,6 +49,7 @@
 
 #include "decode_sm100.cuh"
 #include "fwd_sm100.cuh"
+#include "paged_cache_sm100.cuh"
 #include "ptx_sm100.cuh"
 #include "tmem_wide.cuh"
 
@@ -213,22 +214,6 @@ __device__ __forceinline__ bool paged_warp_wait(uint32_t bar, uint32_t parity,
 }
 
 // ------------------------------------------------------------- schedule --
-struct PagedSeq {
-    int tok, n, len;   // first row, new tokens, cached keys; all clamped to the tensors
-    bool bad;
-};
-
-__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
-    PagedSeq s;
-    const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), l = __ldg(p.seq_lens + b);
-    const int cap = p.max_pages << p.page_shift;
-    s.tok = min(max(c0, 0), p.T);
-    s.n = min(max(c1, s.tok), p.T) - s.tok;
-    s.len = min(max(l, 0), cap);
-    s.bad = s.tok != c0 || s.tok + s.n != c1 || s.len != l;
-    return s;
-}
-
 // a / b for a >= 0, b > 0; the 64-bit division is long, and rarely needed
 __device__ __noinline__ long long div_long(long long a, long long b) { return a / b; }
 __device__ __forceinline__ long long div_fast(long long a, long long b) {

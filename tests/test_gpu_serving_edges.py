@@ -47,3 +47,40 @@ def test_select_infinite_bounds_on_the_side_not_taken(T, ctx):
     sel, status = _select(s, kb, 4, 16)
     assert status == 0
     assert torch.equal(sel, pu.ref_select(s, kb, 4, 0, 0))
+
+
+@pytest.mark.parametrize("what", ["long", "negative", "past_rows", "descending", "before_rows"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_select_reports_bad_lengths_and_offsets(what, new):
+    """Lengths and offsets out of range are clamped as the attention clamps them, and reported; all
+    table entries are good here, so nothing else sets the status."""
+    m = gpu_util.ea()
+    s = pu.make_step([new] * 3, [100 - new] * 3, 4, 2, 64, 16, seed=new, pad=0, poison=False,
+                     extra_pages=0)
+    kb = pu.page_bounds(s.kc)
+    if what == "long":          # a table of 7 pages holds 112 tokens
+        s.seq[1], s.lens[1] = 10 ** 6, 112
+    if what == "negative":
+        s.seq[1], s.lens[1] = -3, 0
+    if what == "past_rows":
+        s.cu[3] = 10 ** 6
+    if what == "before_rows":
+        s.cu[0] = -2            # the first sequence's rows still end where they did
+    if what == "descending":
+        s.cu[1] = s.cu[2] + 1
+    good = s.cu.clone()
+    sel, status = _select(s, kb, 3, 16, 0, 1)
+    assert status == m.ATTN_ERR_BAD_INDEX and m.attn_status() == 0
+    if what == "descending":    # whose rows these are is not defined
+        return
+    s.cu = torch.tensor([0, new, 2 * new, 3 * new], dtype=torch.int32)
+    assert torch.equal(sel, pu.ref_select(s, kb, 3, 0, 1))
+    s.cu = good
+    o, lse = (torch.full((s.T, s.Hq, s.d), -77, dtype=torch.bfloat16, device="cuda"),
+              torch.full((s.T, s.Hq), -77, dtype=torch.float32, device="cuda"))
+    ws = torch.empty(m.attn_fwd_paged_workspace_bytes(64), dtype=torch.uint8, device="cuda")
+    m.attn_sparse_paged(s.q.cuda(), s.kc.cuda(), s.vc.cuda(), s.table.cuda(), s.cu.cuda(),
+                        s.seq.cuda(), sel.cuda(), o, lse, s.scale, ws)
+    assert m.attn_status() == m.ATTN_ERR_BAD_INDEX
+    s.cu = torch.tensor([0, new, 2 * new, 3 * new], dtype=torch.int32)
+    pu.check_attn(s, o.cpu(), lse.cpu(), pu.ref_attn(s, sel=sel), "the same positions")
