@@ -670,16 +670,20 @@ __global__ void __launch_bounds__(kScoreThreads<ROWS>) attn_page_score_kernel(co
                         reinterpret_cast<float*>(p.keys + row * p.max_pages)[page0 + col] = m;
                 }
             }
-            // ---- the error of these sums: 2 D / 16 <= 16 steps that each add 17 numbers, every one
-            // of them cut off below 2^-23 of the largest at worst: under 16 * 17 * 2^-23 < 3.3e-5
-            // times sum |q b| <= |q| |b|, both at least 2^-50 (least_sum), which covers what products
-            // and sums lose below 2^-126 (2 D * 2^-126 <= 2^-118). 0: all scores are exactly 0
+            // ---- the error of these sums. How a product adds up is not documented; assumed is
+            // that it takes steps of w >= 4 terms, each of which cuts its w + 1 numbers (the
+            // terms, and the sum so far) and its result off below 2^-23 of the largest at worst:
+            // (2 D / w) (w + 2) 2^-23 <= 64 * 6 * 2^-23 < 4.6e-5 times sum |q b| <= |q| |b|.
+            // 5e-5 leaves room for the fp32 sums of squares (2^-15 of themselves), the roots and
+            // s +- 2 E below (2^-23 |s|). |q| and |b| are both at least 2^-50 (least_sum), which
+            // covers what products and sums lose below 2^-126 (2 D * 2^-126 <= 2^-118). 0: all
+            // scores are exactly 0
             if (tid < ntok) {
                 float sum = 0.f;
                 for (int h = 0; h < in; ++h) sum = fmaxf(sum, s_sum[tid * p.G + h]);
                 float b = 0.f;
                 for (int w = 0; w < kParts; ++w) b += fmaxf(s_red[2 * w], s_red[2 * w + 1]);
-                float e = sqrtf(sum) * sqrtf(b) * 3.3e-5f;
+                float e = sqrtf(sum) * sqrtf(b) * 5e-5f;
                 float* dst = p.err + ((size_t)(s0 + tid) * p.Hkv + hk) * p.tiles + tile;
                 if (r0 > 0) e = fmaxf(e, *dst);   // this thread's own, of the first heads
                 if (dcheck(s0 + tid < p.T)) *dst = e;

@@ -84,3 +84,53 @@ def test_select_reports_bad_lengths_and_offsets(what, new):
     assert m.attn_status() == m.ATTN_ERR_BAD_INDEX
     s.cu = torch.tensor([0, new, 2 * new, 3 * new], dtype=torch.int32)
     pu.check_attn(s, o.cpu(), lse.cpu(), pu.ref_attn(s, sel=sel), "the same positions")
+
+
+@pytest.mark.parametrize("kind", ["flat", "normal", "exponents", "cancel"])
+@pytest.mark.parametrize("T,Hq,d", [(1, 4, 128), (3, 1, 64), (70, 4, 128), (40, 8, 64)])
+def test_select_scores_are_within_their_error_bound(kind, T, Hq, d):
+    """The fp32 scores and the error bounds that a call leaves in its workspace (rows that may take all
+    their pages are not ranked further) against scores in 64 bits. A bound is no less than what steps
+    of four terms may lose: 2 d / 4 steps cut off 4 + 2 numbers each below 2^-23 of at most |q| |b|;
+    the two norms' own sums are off by 2^-15."""
+    m = gpu_util.ea()
+    s = pu.make_step([T], [1500], Hq, 1, d, 16, seed=T + d, poison=False)
+    pages = -(-s.lens[0] // 16)
+    g = torch.Generator().manual_seed(7)
+    kb = pu.page_bounds(s.kc).double()
+    q = s.q.double()
+    if kind == "flat":              # equal squares: the bound is as tight as it gets
+        q, kb = torch.sign(q) * 1.0078125, torch.sign(kb) * 1.0078125
+    if kind == "exponents":
+        q = q * 2.0 ** torch.randint(-30, 30, q.shape, generator=g)
+        kb = kb * 2.0 ** torch.randint(-30, 30, kb.shape, generator=g)
+    if kind == "cancel":            # large terms of both signs, whose sum is small
+        q = q.abs()
+        kb[..., 0::2], kb[..., 1::2] = kb[..., 0::2].abs() + 100, -kb[..., 1::2].abs() - 100
+    s.q, kb = q.bfloat16(), kb.bfloat16()
+    q, b = s.q.double(), kb[s.table[0, :pages].long(), 0].double()        # [pages, 2, d]
+    want = torch.where(q[:, :, None] >= 0, q[:, :, None] * b[:, 1], q[:, :, None] * b[:, 0]).sum(-1)
+    want = want.amax(1)                                                   # [T, pages]
+    K = s.max_pages
+    ws = torch.zeros(m.attn_page_select_workspace_bytes(T, 1, s.max_pages), dtype=torch.uint8,
+                     device="cuda")
+    sel = torch.full((T, 1, K), -7, dtype=torch.int32, device="cuda")
+    m.attn_page_select(s.q.cuda(), kb.cuda(), s.table.cuda(), s.cu.cuda(), s.seq.cuda(), sel, 16, 0,
+                       0, ws)
+    assert m.attn_status() == 0
+    ws = ws.cpu()
+    tiles = -(-s.max_pages // 64)
+    at = -(-T * s.max_pages * 8 // 256) * 256
+    got = ws[:T * s.max_pages * 8].view(torch.float32).reshape(T, 2 * s.max_pages)[:, :pages].double()
+    err = ws[at:at + T * tiles * 4].view(torch.float32).reshape(T, tiles).double()
+    pos = s.lens[0] - T + torch.arange(T)
+    for tile in range(tiles):
+        part = slice(64 * tile, min(64 * tile + 64, pages))
+        if part.start >= pages:
+            continue
+        norm = (q ** 2).sum(-1).sqrt().amax(1) * (b[part] ** 2).sum((1, 2)).sqrt().amax()
+        least = (2 * d // 4) * 6 * 2.0 ** -23 * norm * (1 - 2.0 ** -15)
+        seen = torch.arange(part.start, part.stop)[None] <= pos[:, None] // 16
+        off = torch.where(seen, (got[:, part] - want[:, part]).abs(), 0.0).amax(1)
+        assert (off <= err[:, tile]).all(), (off / err[:, tile]).max()
+        assert (err[:, tile] >= least).all(), (err[:, tile] / least).min()
