@@ -50,6 +50,7 @@
 #include "decode_sm100.cuh"
 #include "fwd_sm100.cuh"
 #include "paged_cache_sm100.cuh"
+#include "paged_drain.cuh"
 #include "ptx_sm100.cuh"
 #include "tmem_wide.cuh"
 
@@ -593,7 +594,8 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
 
     uint32_t it = 0;                  // key tiles loaded by this CTA
     uint32_t q_used[2] = {0, 0};
-    uint32_t tails = 0, raw_par = 0, raw_last = 0;
+    uint32_t tails = 0, raw_par = 0, raw_last = 0;   // (bits by slot pair, see paged_drain)
+    bool v_skipped = false;           // gave up before the last counted tile's V copy
 
     for (uint32_t units = 0;; ++units) {
         const int ri = units % T::kUnits;
@@ -682,8 +684,8 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
                 }
                 if constexpr (V) {
                     if (round > 0 && !paged_warp_wait(b.kv_empty(sv), (round - 1) & 1, abort_flag)) {
-                        ++it;   // this tile's V is not in flight
-                        raw_last |= 1u << (8 + pair);
+                        ++it;
+                        v_skipped = true;
                         goto fail;
                     }
                     uint32_t vbar = b.kv_full(sv);
@@ -692,7 +694,7 @@ __device__ void paged_producer(const PagedParams& p, const CUtensorMap* tq, cons
                         if (tails >= 2 &&
                             !paged_warp_wait(b.tail_empty(i), ((tails >> 1) - 1) & 1, abort_flag)) {
                             ++it;
-                            raw_last |= 1u << (8 + pair);
+                            v_skipped = true;
                             goto fail;
                         }
                         vbar = b.v_raw(pair);
@@ -739,17 +741,12 @@ fail:
     // flight so that none lands in shared memory after the CTA has exited.
     if (lane == 0) {
         volatile int no_abort = 0;
-        const uint32_t first = it > (uint32_t)T::kPairs ? it - T::kPairs : 0;
-        for (uint32_t i = first; i < it; ++i) {
-            const uint32_t pair = i % T::kPairs, par = (i / T::kPairs) & 1;
-            if (K) paged_wait(b.kv_full(2 * pair), par, &no_abort);
-            const bool no_v = i + 1 == it && ((raw_last >> (8 + pair)) & 1);
-            if (!V || no_v) continue;
-            if ((raw_last >> pair) & 1)
-                paged_wait(b.v_raw(pair), ((raw_par >> pair) & 1) ^ 1, &no_abort);
-            else
-                paged_wait(b.kv_full(2 * pair + 1), par, &no_abort);
-        }
+        paged_drain<K, V>(
+            it, v_skipped, T::kPairs, raw_par, raw_last,
+            [&](uint32_t pair, uint32_t par) { paged_wait(b.kv_full(2 * pair), par, &no_abort); },
+            [&](uint32_t pair, bool raw, uint32_t par) {
+                paged_wait(raw ? b.v_raw(pair) : b.kv_full(2 * pair + 1), par, &no_abort);
+            });
         for (int i = 0; i < 2; ++i)
             if (K && q_used[i] > 0)
                 paged_wait(b.q_full(i), (q_used[i] - 1) & 1, &no_abort);
