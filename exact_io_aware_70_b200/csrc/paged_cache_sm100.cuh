@@ -85,6 +85,12 @@ __device__ __forceinline__ void block_scan(int& v, int& tot, int* red) {
     if (warp > 0) v += before;
 }
 
+// a + b, at most `top`, for a and b in [0, top]: in 32 bits without a sign, as two row counts of
+// 2^30 (the largest T) add up to 2^31.
+__device__ __forceinline__ int sum_to(int a, int b, int top) {
+    return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)top);
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -124,12 +130,11 @@ __global__ void __launch_bounds__(kTablesThreads) attn_page_tables_kernel(const 
         // sums saturate at T: rows past the buffer are cut off, tokens with them
         int end = min(add, p.T), tot;
         {
-            // min(. , T) of a sum of values <= T: scan in 64 bits would do the same
             const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int u = __shfl_up_sync(0xffffffffu, end, off);
-                if (lane >= off) end = min(end + u, p.T);
+                if (lane >= off) end = sum_to(end, u, p.T);
             }
             __syncthreads();
             if (lane == 31) red[warp] = end;
@@ -138,13 +143,13 @@ __global__ void __launch_bounds__(kTablesThreads) attn_page_tables_kernel(const 
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int u = __shfl_up_sync(0xffffffffu, x, off);
-                if (lane >= off) x = min(x + u, p.T);
+                if (lane >= off) x = sum_to(x, u, p.T);
             }
             tot = __shfl_sync(0xffffffffu, x, 31);
             const int before = __shfl_sync(0xffffffffu, x, (warp + 31) & 31);
-            if (warp > 0) end = min(end + before, p.T);
+            if (warp > 0) end = sum_to(end, before, p.T);
         }
-        end = min(end + rows, p.T);
+        end = sum_to(end, rows, p.T);
         // where this sequence's rows begin: the end of the one before
         __syncthreads();
         if (b < p.B) s_cu[b + 1] = end;
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kTablesThreads) attn_page_tables_kernel(const 
             s_ctx[b] = ctx;
             s_page[b] = pages + v - need;
         }
-        rows = min(rows + tot, p.T);
+        rows = sum_to(rows, tot, p.T);
         pages += ptot;
     }
     if (bad) atomicOr(&g_attn_status, bad);

@@ -134,3 +134,25 @@ def test_select_scores_are_within_their_error_bound(kind, T, Hq, d):
         off = torch.where(seen, (got[:, part] - want[:, part]).abs(), 0.0).amax(1)
         assert (off <= err[:, tile]).all(), (off / err[:, tile]).max()
         assert (err[:, tile] >= least).all(), (err[:, tile] / least).min()
+
+
+def test_tables_largest_number_of_rows():
+    """2^30 rows, and sequences that ask for 2^30 tokens each: the first gets them all (two sums of
+    2^30 do not fit 32 bits with a sign)."""
+    m = gpu_util.ea()
+    n, ps, B = 2 ** 30, 1024, 40
+    pages = n // ps
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ctx, new = torch.zeros(B, **i32), torch.full((B,), n, **i32)
+    new[3] = 7
+    head, seq, cu = torch.zeros(1, **i32), torch.zeros(B, **i32), torch.zeros(B + 1, **i32)
+    table = torch.full((B, pages), -5, **i32)
+    slots = torch.empty(n, dtype=torch.int64, device="cuda")
+    m.attn_page_tables(ctx, new, torch.arange(pages, **i32), head, head, table, seq, cu, slots, ps,
+                       pages)
+    assert m.attn_status() == m.ATTN_ERR_BAD_INDEX          # the others' tokens are cut off
+    assert seq.tolist() == [n] + [0] * (B - 1) and cu.tolist() == [0] + [n] * B
+    assert head.item() == pages
+    assert torch.equal(table[0], torch.arange(pages, **i32)) and (table[1:] == -5).all()
+    for at in range(0, n, n // 8):
+        assert torch.equal(slots[at:at + n // 8], torch.arange(at, at + n // 8, device="cuda"))
