@@ -28,6 +28,7 @@ __device__ unsigned g_attn_status = 0;
 #include "fwd_sm100.cuh"
 #include "paged_cache_sm100.cuh"
 #include "paged_fwd_sm100.cuh"
+#include "paged_host.cuh"
 #include "paged_rows_sm100.cuh"
 
 using namespace eattn;
@@ -130,7 +131,7 @@ bool encode_q_map(CUtensorMap* map, const void* base, int T, int Hq, int D, long
 struct DeviceInfo {
     int sms = 0;
     bool paged_attr_set[12] = {};
-    bool tables_attr_set = false;
+    bool tables_attr_set = false, tables_sixteen = false;
     bool score_attr_set[4] = {};
     bool fwd_attr_set[8] = {false, false, false, false, false, false, false, false};
     bool bwd_attr_set[4] = {false, false, false, false};
@@ -849,9 +850,19 @@ attn_status_t attn_page_tables(const int* ctx_lens, const int* new_lens, const i
         return ATTN_ERR_ALIGNMENT;
     const int dev = current_device();
     if (dev < 0 || dev >= 64) return ATTN_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kTablesThreads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int ctas;
     {
         std::lock_guard<std::mutex> lk(g_dev_mu);
-        if (!g_dev[dev].tables_attr_set) {
+        DeviceInfo& di = g_dev[dev];
+        if (!di.tables_attr_set) {
             if (cudaFuncSetAttribute(attn_page_tables_kernel,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (3 * kTablesMaxSeqs + 1) * 4) != cudaSuccess ||
@@ -859,29 +870,27 @@ attn_status_t attn_page_tables(const int* ctx_lens, const int* new_lens, const i
                                      cudaFuncAttributeNonPortableClusterSizeAllowed,
                                      1) != cudaSuccess)
                 return ATTN_ERR_CUDA;
-            g_dev[dev].tables_attr_set = true;
+            // whether this process has room for a cluster of 16 (an answer of no, or none: 8 will do)
+            cfg.gridDim = dim3(16);
+            cfg.dynamicSmemBytes = (3 * kTablesMaxSeqs + 1) * 4;
+            attr[0].val.clusterDim.x = 16;
+            int fit = 0;
+            if (cudaOccupancyMaxActiveClusters(&fit, attn_page_tables_kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                fit = 0;
+            }
+            di.tables_sixteen = fit > 0;
+            di.tables_attr_set = true;
         }
+        ctas = tables_ctas(T, kTablesThreads, di.tables_sixteen);
     }
     TablesParams p{ctx_lens, new_lens,  free_pages, free_head, free_head_out,
                    block_table, seq_lens, cu_q,     slot_map,  B,
                    T,        num_free,  shift_of(page_size), max_pages_per_seq, num_pages};
-    // as many CTAs as there are rows for, up to the largest cluster
-    const int ctas = T <= kTablesThreads       ? 1
-                     : T <= 2 * kTablesThreads ? 2
-                     : T <= 8 * kTablesThreads ? 8
-                                               : 16;
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kTablesThreads);
     cfg.dynamicSmemBytes = (size_t)(3 * B + 1) * 4;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, attn_page_tables_kernel, p) != cudaSuccess) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;
