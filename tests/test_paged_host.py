@@ -1,4 +1,4 @@
-"""Host-side choices of the serving entry points, compiled without CUDA."""
+"""Host-side choices and checks of the serving entry points (no GPU needed)."""
 import ctypes
 import os
 import subprocess
@@ -33,3 +33,44 @@ def test_block_tables_take_no_cluster_that_does_not_fit(lib, rows):
     narrow, wide = lib.ctas(rows, 1024, 0), lib.ctas(rows, 1024, 1)
     assert narrow in (1, 2, 8) and narrow == min(wide, 8)
     assert wide == (1 if rows <= 1024 else 2 if rows <= 2048 else 8 if rows <= 8192 else 16)
+
+
+@pytest.mark.parametrize("what", ["page_size", "num_pages", "negative", "rows", "free", "keep_first",
+                                  "keep_last", "select_page_size", "num_sel", "max_pages"])
+def test_sizes_beyond_32_bits_are_refused(what, monkeypatch):
+    """The C calls take sizes as 32-bit ints: 2^32 + 16 must not pass as 16."""
+    import torch
+
+    import exact_io_aware_70_b200 as ea
+
+    big = 2 ** 32 + 16
+    monkeypatch.setattr(ea, "_pointers", lambda what, names, dtypes, ts: (0, [0x10000] * len(ts)))
+    monkeypatch.setattr(ea, "_rows", lambda t, name, dev: (0x10000, t.shape[1] * t.shape[2]))
+    launched = []
+    monkeypatch.setattr(ea, "_launch", lambda fn, name, dev, args, stream: launched.append(args))
+
+    def i32(*shape):
+        return torch.zeros((1,) * len(shape), dtype=torch.int32).expand(*shape)
+
+    def tables(page_size=16, num_pages=50, rows=4, free=50):
+        ea.attn_page_tables(i32(2), i32(2), i32(free), i32(1), i32(1), i32(2, 8), i32(2), i32(3),
+                            i32(rows), page_size, num_pages)
+
+    def select(keep_first=0, keep_last=1, page_size=16, num_sel=4, max_pages=8):
+        q, kb = torch.zeros((4, 2, 64)), torch.zeros((50, 1, 2, 64))
+        ea.attn_page_select(q, kb, i32(2, max_pages), i32(3), i32(2), i32(4, 1, num_sel), page_size,
+                            keep_first, keep_last, i32(256))
+
+    tables()
+    select()
+    assert len(launched) == 2                    # these pass
+    with pytest.raises(ValueError, match="32 bits"):
+        {"page_size": lambda: tables(page_size=big), "num_pages": lambda: tables(num_pages=big),
+         "negative": lambda: tables(page_size=16 - 2 ** 32), "rows": lambda: tables(rows=big),
+         "free": lambda: tables(free=big), "keep_first": lambda: select(keep_first=big - 16),
+         "keep_last": lambda: select(keep_last=1 - 2 ** 32),
+         "select_page_size": lambda: select(page_size=big), "num_sel": lambda: select(num_sel=big),
+         "max_pages": lambda: select(max_pages=big)}[what]()
+    assert len(launched) == 2
+    with pytest.raises(ValueError, match="32 bits"):
+        ea.attn_page_select_workspace_bytes(4, 2, big)
