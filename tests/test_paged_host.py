@@ -74,3 +74,14 @@ def test_sizes_beyond_32_bits_are_refused(what, monkeypatch):
     assert len(launched) == 2
     with pytest.raises(ValueError, match="32 bits"):
         ea.attn_page_select_workspace_bytes(4, 2, big)
+
+
+def test_smoke_runs_the_serving_step_without_the_test_modules():
+    """The step of smoke() needs helper modules alone, not the tests (nor pytest)."""
+    import ast
+    tree = ast.parse(open(os.path.join(ROOT, "__graft_entry__.py")).read())
+    fn = next(f for f in tree.body if getattr(f, "name", "") == "_smoke_serving")
+    names = {a.name for n in ast.walk(fn) if isinstance(n, (ast.Import, ast.ImportFrom))
+             for a in n.names}
+    assert names == {"torch", "exact_io_aware_70_b200", "paged_util"}
+    assert "test_gpu_serving" not in ast.unparse(tree)
