@@ -332,9 +332,10 @@ def _launch(fn, what: str, dev: int, args, stream) -> None:
         raise AttnError(code, what)
 
 
-def _fit(what: str, *sizes) -> None:
-    """Refuses sizes that the C calls' 32-bit arguments do not hold (ctypes would cut them off)."""
-    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+def _fit(what: str, sizes: int) -> None:
+    """Refuses sizes that the C calls' 32-bit arguments do not hold (ctypes would cut them off).
+    `sizes`: all of a call's or-ed together (where one is negative, the C call refuses it)."""
+    if sizes >> 31 not in (0, -1):
         raise ValueError(f"{what}: sizes beyond 32 bits")
 
 
@@ -372,10 +373,11 @@ def attn_page_tables(ctx_lens, new_lens, free_pages, free_head, free_head_out, b
             or free_pages.dim() != 1 or slot_map.dim() != 1 or free_head.numel() != 1 \
             or free_head_out.numel() != 1:
         raise ValueError("attn_page_tables: inconsistent shapes")
-    sizes = (B, slot_map.numel(), free_pages.numel(), int(page_size), block_table.shape[1],
-             int(num_pages))
-    _fit("attn_page_tables", *sizes)
-    _launch(lib.attn_page_tables, "attn_page_tables", dev, (*ptrs, *sizes), stream)
+    T, F, page_size, max_pages, num_pages = (slot_map.numel(), free_pages.numel(), int(page_size),
+                                             block_table.shape[1], int(num_pages))
+    _fit("attn_page_tables", B | T | F | page_size | max_pages | num_pages)
+    _launch(lib.attn_page_tables, "attn_page_tables", dev,
+            (*ptrs, B, T, F, page_size, max_pages, num_pages), stream)
 
 
 def attn_paged_append(k, v, slot_map, k_cache, v_cache, k_bounds=None, stream=None) -> None:
@@ -410,13 +412,13 @@ def attn_fwd_paged_workspace_bytes(d: int) -> int:
     return int(lib.attn_fwd_paged_workspace_bytes(d))
 
 
-def _check_step(what: str, q, block_table, cu_q, seq_lens, *sizes) -> int:
+def _check_step(what: str, q, block_table, cu_q, seq_lens, sizes: int = 0) -> int:
     """The number of sequences, once the shapes that all calls on q share agree."""
     B = seq_lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B or cu_q.shape != (B + 1,) \
             or seq_lens.dim() != 1:
         raise ValueError(f"{what}: inconsistent shapes")
-    _fit(what, B, q.shape[0], block_table.shape[1], *sizes)
+    _fit(what, B | q.shape[0] | block_table.shape[1] | sizes)
     return B
 
 
@@ -444,7 +446,7 @@ def attn_fwd_paged(q, k_cache, v_cache, block_table, cu_q, seq_lens, o, lse, cau
 
 
 def attn_page_select_workspace_bytes(T: int, Hkv: int, max_pages: int) -> int:
-    _fit("attn_page_select_workspace_bytes", T, Hkv, max_pages)
+    _fit("attn_page_select_workspace_bytes", T | Hkv | max_pages)
     return int(lib.attn_page_select_workspace_bytes(T, Hkv, max_pages))
 
 
@@ -461,11 +463,11 @@ def attn_page_select(q, k_bounds, block_table, cu_q, seq_lens, sel, page_size: i
     qp, qs = _rows(q, "q", dev)
     T, Hq, d = q.shape
     keep_first, keep_last, page_size = int(keep_first), int(keep_last), int(page_size)
-    B = _check_step("attn_page_select", q, block_table, cu_q, seq_lens, *sel.shape, keep_first,
-                    keep_last, page_size)
     if k_bounds.dim() != 4 or k_bounds.shape[2:] != (2, d) or sel.dim() != 3 \
             or sel.shape[:2] != (T, k_bounds.shape[1]):
         raise ValueError("attn_page_select: inconsistent shapes")
+    B = _check_step("attn_page_select", q, block_table, cu_q, seq_lens,
+                    sel.shape[2] | keep_first | keep_last | page_size)
     _launch(lib.attn_page_select, "attn_page_select", dev,
             (qp, *ptrs[:5], B, T, Hq, k_bounds.shape[1], d, sel.shape[2], keep_first,
              keep_last, qs, page_size, block_table.shape[1], k_bounds.shape[0], ptrs[5],
@@ -483,11 +485,11 @@ def attn_sparse_paged(q, k_cache, v_cache, block_table, cu_q, seq_lens, sel, o, 
                           (k_cache, v_cache, block_table, cu_q, seq_lens, sel, o, lse, workspace))
     qp, qs = _rows(q, "q", dev)
     T, Hq, d = q.shape
-    B = _check_step("attn_sparse_paged", q, block_table, cu_q, seq_lens, *sel.shape)
     if k_cache.dim() != 4 or k_cache.shape[3] != d or v_cache.shape != k_cache.shape \
             or o.shape != q.shape or lse.shape != (T, Hq) or sel.dim() != 3 \
             or sel.shape[:2] != (T, k_cache.shape[1]):
         raise ValueError("attn_sparse_paged: inconsistent shapes")
+    B = _check_step("attn_sparse_paged", q, block_table, cu_q, seq_lens, sel.shape[2])
     P, Hkv, page_size, _ = k_cache.shape
     _launch(lib.attn_sparse_paged, "attn_sparse_paged", dev,
             (qp, *ptrs[:8], B, T, Hq, Hkv, d, sel.shape[2], qs, page_size, block_table.shape[1], P,
