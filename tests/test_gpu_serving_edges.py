@@ -1,4 +1,6 @@
 """Calls of the serving operators at the edges of what their documentation allows."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -156,3 +158,195 @@ def test_tables_largest_number_of_rows():
     assert torch.equal(table[0], torch.arange(pages, **i32)) and (table[1:] == -5).all()
     for at in range(0, n, n // 8):
         assert torch.equal(slots[at:at + n // 8], torch.arange(at, at + n // 8, device="cuda"))
+
+
+def _attn(s, causal=True, sel=None):
+    m = gpu_util.ea()
+    o = torch.full((s.T, s.Hq, s.d), -77, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((s.T, s.Hq), -77, dtype=torch.float32, device="cuda")
+    ws = torch.empty(m.attn_fwd_paged_workspace_bytes(s.d), dtype=torch.uint8, device="cuda")
+    a = (s.q.cuda(), s.kc.cuda(), s.vc.cuda(), s.table.cuda(), s.cu.cuda(), s.seq.cuda())
+    if sel is None:
+        m.attn_fwd_paged(*a, o, lse, causal, s.scale, ws)
+    else:
+        m.attn_sparse_paged(*a, sel.cuda(), o, lse, s.scale, ws)
+    return o.cpu(), lse.cpu(), m.attn_status()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("N,H,d,ps", [(1, 3, 64, 16), (700, 4, 128, 64), (1025, 2, 64, 32)])
+def test_prompt_agrees_with_the_dense_forward(N, H, d, ps, causal):
+    """A whole prompt, nothing cached before: attn_fwd and attn_fwd_paged are both within the bounds
+    of the 64-bit definition, and so within twice those of each other."""
+    m = gpu_util.ea()
+    s = pu.make_step([N], [0], H, H, d, ps, seed=N + d)
+    o, lse, status = _attn(s, causal)
+    assert status == 0
+    ref = pu.ref_attn(s, causal)
+    pu.check_attn(s, o, lse, ref, "paged")
+    k, v, _ = pu.seq_kv(s, 0)
+    q = s.q.transpose(0, 1)[None].contiguous().cuda()
+    od = torch.empty_like(q)
+    ld = torch.empty((1, H, N), dtype=torch.float32, device="cuda")
+    m.attn_fwd(q, k.bfloat16()[None].contiguous().cuda(), v.bfloat16()[None].contiguous().cuda(), od,
+               ld, causal, s.scale)
+    assert m.attn_status() == 0
+    od, ld = od[0].transpose(0, 1).cpu(), ld[0].T.cpu()
+    pu.check_attn(s, od, ld, ref, "dense")
+    assert ((o.double() - od.double()).abs() <= 2 * ref[2]).all()
+    assert ((lse.double() - ld.double()).abs() <= 2 * ref[3]).all()
+
+
+def test_append_bounds_beyond_31_bits():
+    """The last slot of a cache of more than 2^31 elements: both bounds are those of the whole page,
+    and no other page's change."""
+    m = gpu_util.ea()
+    ps, Hkv, d = 1024, 8, 128
+    pages = 2 ** 31 // (ps * Hkv * d) + 3
+    kc, vc = (torch.empty((pages, Hkv, ps, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kc[-1] = torch.randn((Hkv, ps, d), device="cuda").bfloat16()
+    kb = torch.full((pages, Hkv, 2, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.randn((1, Hkv, d), device="cuda").bfloat16() for _ in range(2))
+    m.attn_paged_append(k, v, torch.tensor([pages * ps - 1], device="cuda"), kc, vc, kb)
+    assert m.attn_status() == 0
+    assert torch.equal(kc[-1, :, -1], k[0]) and torch.equal(vc[-1, :, -1], v[0])
+    assert torch.equal(kb[-1, :, 0], kc[-1].amin(1)) and torch.equal(kb[-1, :, 1], kc[-1].amax(1))
+    assert (kb[:-1] == 3).all()
+
+
+@pytest.mark.parametrize("B,Hkv,new", [(3, 1, 1), (3, 2, 5), (40, 1, 1)])
+def test_choice_right_behind_the_tables(B, Hkv, new):
+    """A captured step whose page choice follows the kernel that writes its lengths, offsets and tables:
+    replay after replay the choice goes by that replay's, although it looks rows up early."""
+    m = gpu_util.ea()
+    ps, d, K, max_pages, replays = 16, 64, 4, 24, 60
+    num_pages = B * max_pages + 7
+    g = torch.Generator().manual_seed(B + new)
+    free = torch.randperm(num_pages, generator=g).tolist()
+    kb = torch.randn((num_pages, Hkv, 2, d), generator=g)
+    kb = torch.stack([kb.amin(2), kb.amax(2)], 2).bfloat16()
+    q = torch.randn((B * new, 2 * Hkv, d), generator=g).bfloat16()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    start = [7 * b % 30 for b in range(B)]
+    table = [[-1] * max_pages for _ in range(B)]
+    for b in range(B):
+        for i in range(-(-start[b] // ps)):
+            table[b][i] = free.pop()
+    lens, dnew = torch.tensor(start, **i32), torch.full((B,), new, **i32)
+    dtab, dfree, head = torch.tensor(table, **i32), torch.tensor(free, **i32), torch.zeros(1, **i32)
+    cu, slots = torch.zeros(B + 1, **i32), torch.zeros(B * new, dtype=torch.int64, device="cuda")
+    dq, dkb = q.cuda(), kb.cuda()
+    sel = torch.full((B * new, Hkv, K), -7, **i32)
+    ws = torch.empty(m.attn_page_select_workspace_bytes(B * new, Hkv, max_pages), dtype=torch.uint8,
+                     device="cuda")
+    seen = torch.full((replays, B * new, Hkv, K), -9, **i32)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            m.attn_page_tables(lens, dnew, dfree, head, head, dtab, lens, cu, slots, ps, num_pages)
+            m.attn_page_select(dq, dkb, dtab, cu, lens, sel, ps, 1, 1, ws)
+        for i in range(replays):
+            graph.replay()
+            seen[i].copy_(sel)
+        assert m.attn_status() == 0
+    seen = seen.cpu()
+    at, taken = list(start), 0
+    for i in range(replays):
+        table, at, wcu, _, taken, fine = pu.ref_tables(at, [new] * B, free, taken, table, B * new, ps,
+                                                       num_pages)
+        assert fine
+        s = SimpleNamespace(T=B * new, Hq=2 * Hkv, Hkv=Hkv, B=B, new=[new] * B, lens=at, ps=ps, q=q,
+                            cu=torch.tensor(wcu), table=torch.tensor(table), num_pages=num_pages)
+        assert torch.equal(seen[i], pu.ref_select(s, kb, K, 1, 1)), f"replay {i}"
+
+
+@pytest.mark.parametrize("ps,K,Hq", [(16, 480, 4), (64, 480, 1), (128, 480, 8), (256, 240, 2),
+                                     (1024, 60, 4)])
+def test_sparse_longest_lists(ps, K, Hq):
+    """As many pages in a row's list as the call takes, all of them there, in any order."""
+    m = gpu_util.ea()
+    s = pu.make_step([1, 2], [(K + 3) * ps - 5, 40], Hq, 1, 64, ps, seed=K + ps)
+    g = torch.Generator().manual_seed(ps)
+    sel = torch.full((3, 1, K), -1, dtype=torch.int32)
+    sel[0, 0] = torch.randperm(K + 3, generator=g)[:K].int()
+    sel[1, 0, K - 1], sel[2, 0, 0] = 0, 0
+    o, lse, status = _attn(s, sel=sel)
+    assert status == 0
+    pu.check_attn(s, o, lse, pu.ref_attn(s, sel=sel), "long lists")
+    with pytest.raises(m.AttnError):
+        _attn(s, sel=torch.full((3, 1, K + 1), -1, dtype=torch.int32))
+
+
+def test_select_largest_table():
+    """16384 pages, the most that the choice takes."""
+    s = pu.make_step([2], [16384 * 16 - 2], 2, 1, 64, 16, seed=8, poison=False, extra_pages=0)
+    assert s.max_pages == 16384
+    kb = pu.page_bounds(s.kc)
+    sel, status = _select(s, kb, 40, 16, 1, 2)
+    assert status == 0 and torch.equal(sel, pu.ref_select(s, kb, 40, 1, 2))
+    s.table, s.max_pages = torch.cat([s.table, s.table[:, :1]], 1), 16385
+    with pytest.raises(gpu_util.ea().AttnError):
+        _select(s, kb, 40, 16, 1, 2)
+
+
+@pytest.mark.parametrize("new,ctx", [([1, 1, 1], [700, 15, 16]), ([4, 0, 3], [300, 9, 2000])])
+def test_mostly_padding_rows(new, ctx):
+    """A step in a buffer made for far more rows than it has."""
+    s = pu.make_step(new, ctx, 8, 2, 128, 32, seed=3, pad=3000)
+    o, lse, status = _attn(s)
+    assert status == 0
+    pu.check_attn(s, o, lse, pu.ref_attn(s), "padded")
+    kb = pu.page_bounds(torch.nan_to_num(s.kc))
+    sel, status = _select(s, kb, 5, 32, 1, 1)
+    assert status == 0 and torch.equal(sel, pu.ref_select(s, kb, 5, 1, 1))
+    o, lse, status = _attn(s, sel=sel)
+    assert status == 0
+    pu.check_attn(s, o, lse, pu.ref_attn(s, sel=sel), "padded, chosen pages")
+
+
+def test_captured_behind_a_join():
+    """A captured step that follows work on two streams, a copy and a fill (the launches overlap only
+    what they may)."""
+    m = gpu_util.ea()
+    s = pu.make_step([1, 30], [900, 77], 8, 2, 64, 16, seed=6, pad=1)
+    kb = pu.page_bounds(torch.nan_to_num(s.kc))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    src = (s.q.cuda(), s.kc.cuda(), s.vc.cuda())
+    q, kc, vc = (torch.zeros_like(x) for x in src)
+    table, cu, seq, dkb = s.table.cuda(), s.cu.cuda(), s.seq.cuda(), kb.cuda()
+    o, o2 = (torch.zeros((s.T, 8, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse, lse2 = (torch.zeros((s.T, 8), dtype=torch.float32, device="cuda") for _ in range(2))
+    sel = torch.zeros((s.T, 2, 6), **i32)
+    ws = torch.empty(m.attn_fwd_paged_workspace_bytes(64), dtype=torch.uint8, device="cuda")
+    ws2 = torch.empty(m.attn_page_select_workspace_bytes(s.T, 2, s.max_pages), dtype=torch.uint8,
+                      device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            kc.copy_(src[1])
+            vc.copy_(src[2])
+        q.copy_(src[0])
+        for x in (o, o2, lse, lse2):
+            x.fill_(-77)
+        sel.fill_(-7)
+        main.wait_stream(side)
+        m.attn_fwd_paged(q, kc, vc, table, cu, seq, o, lse, True, s.scale, ws)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            m.attn_page_select(q, dkb, table, cu, seq, sel, 16, 1, 1, ws2)
+        main.wait_stream(side)
+        m.attn_sparse_paged(q, kc, vc, table, cu, seq, sel, o2, lse2, s.scale, ws)
+        kc.zero_()
+        q.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert m.attn_status() == 0
+    pu.check_attn(s, o.cpu(), lse.cpu(), pu.ref_attn(s), "joined")
+    want = pu.ref_select(s, kb, 6, 1, 1)
+    assert torch.equal(sel.cpu(), want)
+    pu.check_attn(s, o2.cpu(), lse2.cpu(), pu.ref_attn(s, sel=want), "joined, chosen pages")
