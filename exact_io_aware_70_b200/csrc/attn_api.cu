@@ -77,55 +77,56 @@ EncodeTiledFn get_encode_fn() {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Encodes a 3-D tiled map whose rows beyond the tensor read as zero. The driver call needs a
+// current context, which a host thread gets with its first runtime call that uses the device:
+// where this is the thread's first call of all, the device's context is made current first.
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, const void* base,
+                  const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+                  const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    auto encode = [&] {
+        return enc(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    if (r != CUDA_SUCCESS && r != CUDA_ERROR_INVALID_VALUE) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+    }
+    return r == CUDA_SUCCESS;
+}
+
 // Tensor map over a bf16 tensor viewed as [BH][N][D]; box = box_rows rows x 64
 // columns, 128-byte swizzle, out-of-range rows read as zero.
 bool encode_bf16_map(CUtensorMap* map, const void* base, int BH, int N, int D,
                      int box_rows = 128) {
-    EncodeTiledFn enc = get_encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH};
-    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
+                        {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH},
+                        {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2}, {64, (cuuint32_t)box_rows, 1},
+                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Tensor map over an 8-bit tensor viewed as [BH][N][D] with D = 128 or 64: box =
 // 128 rows x D bytes, 128-byte swizzle (64-byte swizzle for D = 64), rows past
 // N read as zero.
 bool encode_u8_map(CUtensorMap* map, const void* base, int BH, int N, int D) {
-    EncodeTiledFn enc = get_encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH};
-    cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)N * D};
-    cuuint32_t box[3] = {(cuuint32_t)D, 128, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
-                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base,
+                        {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH},
+                        {(cuuint64_t)D, (cuuint64_t)N * D}, {(cuuint32_t)D, 128, 1},
+                        D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Tensor map over q viewed as [T][Hq][D] with `stride` elements from row to row;
 // box = `tokens` rows x the `heads` query heads of a group x 64 columns.
 bool encode_q_map(CUtensorMap* map, const void* base, int T, int Hq, int D, long long stride,
                   int heads, int tokens) {
-    EncodeTiledFn enc = get_encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
-    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
+                        {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T},
+                        {(cuuint64_t)D * 2, (cuuint64_t)stride * 2},
+                        {64, (cuuint32_t)heads, (cuuint32_t)tokens}, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 struct DeviceInfo {

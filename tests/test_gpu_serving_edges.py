@@ -1,4 +1,5 @@
 """Calls of the serving operators at the edges of what their documentation allows."""
+from concurrent.futures import ThreadPoolExecutor
 from types import SimpleNamespace
 
 import pytest
@@ -350,3 +351,68 @@ def test_captured_behind_a_join():
     want = pu.ref_select(s, kb, 6, 1, 1)
     assert torch.equal(sel.cpu(), want)
     pu.check_attn(s, o2.cpu(), lse2.cpu(), pu.ref_attn(s, sel=want), "joined, chosen pages")
+
+
+def test_calls_from_several_threads():
+    """Host threads that call at the same time, each on a stream and a workspace of its own; the call
+    is the first that a thread makes of CUDA at all."""
+    m = gpu_util.ea()
+    steps = [pu.make_step([1, 5, 40][i % 3:][:2] + [1], [300, 70, 900][:len([1, 5, 40][i % 3:][:2]) + 1],
+                          4, 2, 64, 16, seed=i) for i in range(6)]
+    data = [tuple(x.cuda() for x in (s.q, s.kc, s.vc, s.table, s.cu, s.seq)) for s in steps]
+    outs = [(torch.full((s.T, 4, 64), -77, dtype=torch.bfloat16, device="cuda"),
+             torch.full((s.T, 4), -77, dtype=torch.float32, device="cuda"),
+             torch.empty(m.attn_fwd_paged_workspace_bytes(64), dtype=torch.uint8, device="cuda"))
+            for s in steps]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+
+    def work(i):
+        o, lse, ws = outs[i]
+        for _ in range(20):
+            m.attn_fwd_paged(*data[i], o, lse, True, steps[i].scale, ws,
+                             stream=streams[i].cuda_stream)
+
+    with ThreadPoolExecutor(len(steps)) as pool:
+        list(pool.map(work, range(len(steps))))
+    torch.cuda.synchronize()
+    assert m.attn_status() == 0
+    for s, (o, lse, _) in zip(steps, outs):
+        pu.check_attn(s, o.cpu(), lse.cpu(), pu.ref_attn(s), "threads")
+
+
+@pytest.mark.parametrize("what", ["fwd_paged", "sparse", "select", "append", "tables", "fwd", "bwd"])
+def test_first_call_of_a_thread(what):
+    """Every kind of call as the first that a host thread makes of CUDA."""
+    m = gpu_util.ea()
+    s = pu.make_step([3, 1], [60, 5], 2, 2, 64, 16, seed=2)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q, kc, vc, table, cu, seq = (x.cuda() for x in (s.q, s.kc, s.vc, s.table, s.cu, s.seq))
+    o, lse = torch.empty_like(q), torch.empty((4, 2), dtype=torch.float32, device="cuda")
+    sel = torch.zeros((4, 2, 3), **i32)
+    kb = pu.page_bounds(torch.nan_to_num(s.kc)).cuda()
+    ws, ws2 = (torch.empty(n, dtype=torch.uint8, device="cuda")
+               for n in (m.attn_fwd_paged_workspace_bytes(64),
+                         m.attn_page_select_workspace_bytes(4, 2, s.max_pages)))
+    slots, head = torch.arange(4, device="cuda"), torch.zeros(1, **i32)
+    ones, free, offsets = torch.ones(2, **i32), torch.arange(9, **i32), torch.zeros(3, **i32)
+    dense = [torch.randn((1, 2, 40, 64), device="cuda").bfloat16() for _ in range(8)]
+    dl = torch.zeros((1, 2, 40), dtype=torch.float32, device="cuda")
+    wb = torch.empty(m.attn_bwd_workspace_bytes(1, 2, 40, 64), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    call = {
+        "fwd_paged": lambda: m.attn_fwd_paged(q, kc, vc, table, cu, seq, o, lse, True, s.scale, ws,
+                                              stream=stream),
+        "sparse": lambda: m.attn_sparse_paged(q, kc, vc, table, cu, seq, sel, o, lse, s.scale, ws,
+                                              stream=stream),
+        "select": lambda: m.attn_page_select(q, kb, table, cu, seq, sel, 16, 0, 1, ws2, stream=stream),
+        "append": lambda: m.attn_paged_append(q, q, slots, kc, vc, kb, stream=stream),
+        "tables": lambda: m.attn_page_tables(seq, ones, free, head, head, table, seq, offsets, slots,
+                                             16, s.num_pages, stream=stream),
+        "fwd": lambda: m.attn_fwd(*dense[:4], dl, True, s.scale, stream=stream),
+        "bwd": lambda: m.attn_bwd(*dense[:5], dl, *dense[5:], True, s.scale, wb, stream=stream),
+    }[what]
+    with ThreadPoolExecutor(1) as pool:
+        pool.submit(call).result()
+    assert m.attn_status() == 0
