@@ -291,7 +291,8 @@ def test_select_largest_table():
         _select(s, kb, 40, 16, 1, 2)
 
 
-@pytest.mark.parametrize("new,ctx", [([1, 1, 1], [700, 15, 16]), ([4, 0, 3], [300, 9, 2000])])
+@pytest.mark.parametrize("new,ctx", [([1, 1, 1], [700, 15, 16]), ([4, 0, 3], [300, 9, 2000]),
+                                     ([1, 2], [12000, 9000])])
 def test_mostly_padding_rows(new, ctx):
     """A step in a buffer made for far more rows than it has."""
     s = pu.make_step(new, ctx, 8, 2, 128, 32, seed=3, pad=3000)
