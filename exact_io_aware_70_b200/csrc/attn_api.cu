@@ -788,8 +788,13 @@ attn_status_t paged_entry(const void* q, const void* k_cache, const void* v_cach
         return ATTN_ERR_ALIGNMENT;
 
     PagedParams p;
-    // Rows of a unit: with few tokens per sequence (on average; the lengths are on the
-    // device) the turned kernel, whose work follows the rows in use, else 128-row tiles.
+    // Rows of a unit: with few tokens per sequence the turned kernel, whose work follows the rows
+    // in use, else 128-row tiles. One form for the whole call, by the average, as the lengths are
+    // on the device. 16 columns / 32 / 128-row tiles, 16 sequences of 4,000 keys, 32 heads on 8:
+    // 4 rows 54.4 / 53.3 / 58.4 us, 32 rows 92.8 / 55.9 / 60.6, 64 rows 168 / 94 / 64, 128 rows
+    // 292 / 170 / 72; 7 drafts of 42 rows: - / 24.9 / 25.0. (So from 33 rows on 128-row tiles are as
+    // fast or faster; and sequences far from the average pay: 256 that decode at 2,048 keys and a
+    // chunk of 512 tokens behind 8,000 take 610 us in one call, 331 and 100 apart.)
     const long long avg = sel ? 1 : (T + (long long)B - 1) / B;
     const int rows = avg * G <= 16 ? 16 : G <= 32 && avg * G <= 64 ? 32 : 0;
     p.tpt = sel ? 1 : (rows ? rows : 128) / G;
@@ -924,6 +929,12 @@ attn_status_t attn_paged_append(const void* k, const void* v, const long long* s
     p.Hkv = Hkv;
     p.page_shift = shift_of(page_size);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // Rows of a block. 32 of them share a block's launch and copy together, but the pages that end
+    // among them are taken one after another; one row a block spreads those. The host does not
+    // know how many rows share a page, so small calls are taken for decode (every row ends its
+    // page) and large ones for prompts. One row / 32, 8 heads of 128: decode 16 rows 3.8 / 20.6
+    // us, 256 rows 10.7 / 47, 1,024 rows 41 / 74; consecutive rows 128: 4.6 / 4.2, 1,024: 12.5 /
+    // 4.8, 4,095: 31.6 / 6.8, 4,096: 41.9 / 9.6.
     const bool many = (long long)T * Hkv >= 32768;
     const dim3 grid(many ? (T + 31) / 32 : T, Hkv);
     if (d == 128) {
@@ -1078,7 +1089,10 @@ attn_status_t attn_page_select(const void* q, const void* k_bounds, const int* b
                                      round256((size_t)T * Hkv * max_pages_per_seq * 8));
     p.tiles = score_tiles(max_pages_per_seq);
     // 64 tokens share a tile's read of the bounds (the choice for 1,098 tokens: 56 us; 48, 32 or 16
-    // tokens: 61, 58, 62); where sequences have a token or two, one (its pages are its own)
+    // tokens: 61, 58, 62), one sequence after another; where sequences have a token or two, one (its
+    // pages are its own). 1 token / 64, 16 sequences of 512 pages: 1 token each 23 / 78 us, 2: 32 /
+    // 80, 4: 49 / 81, 8: 84 / 54; 64 sequences of 125 pages: 1: 25 / 279, 4: 48 / 85; one
+    // sequence of 256 tokens and 250 pages: 75 / 33.5
     p.tile_tok = (long long)T <= 2ll * B ? 1 : 64;
     p.q_stride = q_stride;
     p.B = B;

@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kAppendThreads) attn_paged_append_kernel(const
 //      the few between are scored again in fp64 (where the sum of a row's exact products
 //      is all but exact) and the best of them fill up the choice.
 // Scoring every page in fp64 ran 287 us on 1098 rows x 8 K/V heads x up to 246 pages
-// (0.8e9 terms for 32 query heads); this way the choice takes 54.
+// (0.8e9 terms for 32 query heads); this way the choice takes 55.
 struct SelectParams {
     const uint16_t* q;          // bf16 [T, Hq, D], q_stride elements from row to row
     const uint16_t* bounds;     // bf16 [num_pages, Hkv, 2, D]

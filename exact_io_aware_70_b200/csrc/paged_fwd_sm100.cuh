@@ -37,11 +37,13 @@
 //     last token may be anything (NaN too): its scores are replaced, and its V
 //     rows are zeroed in shared memory by a warp of their own before P V.
 //
-// Few rows per sequence go to paged_rows_sm100.cuh instead. Measured (CUDA graph, 2 sequences of
-// 2048 and 957 new tokens behind 14.3K and 11.3K keys, 32 query heads on 8, d = 128): 700 us,
-// 1000 TFLOP/s of the visible pairs. What bounds it is the issuing thread, as in the dense
+// Few rows per sequence go to paged_rows_sm100.cuh instead. Measured (2 sequences of 2048 and 957
+// new tokens behind 14.3K and 11.3K keys, 32 query heads on 8, d = 128): 700 us, 1000 TFLOP/s of
+// the visible pairs, in a burst of a dozen launches, 784 us and 893 TFLOP/s under the power limit of
+// longer runs. On the dense forward's own shape (32 heads of 128, 8192 tokens, causal) it takes 661
+// us (678 sustained), that one 488 (541). What bounds it is the issuing thread, as in the dense
 // forward (a product costs it about 0.48 us of queueing for 0.27 us of tensor time), and on short
-// prompts (8 of up to 1024 tokens, 12 heads of 64: 55 us) the start of units and
+// prompts (8 of up to 1024 tokens, 12 heads of 64: 50-54 us) the start of units and
 // the instruction fetch of code that runs a few times only.
 #pragma once
 

@@ -24,9 +24,10 @@
 // Warps: 0-3 and 4-7 softmax, 8 loads Q and K, 13 V, 9 and 11 issue the products of
 // group 0 and 1, 10 cleans V tiles, 12 plans. Measured (CUDA graph): 16 sequences of 32768
 // keys, 32 query heads on 8, 327 us = 6.57 TB/s of K/V, the card's copy rate (128-row form:
-// 354); 1098 rows over 16 pages of 64 each, 553 us = 8.3 TB/s, mostly out of L2, bound by the
-// loads' latency with three tile pairs in flight and by units that are 8 tiles long
-// (1449); 7 sequences of up to 6 drafted tokens, 25 us, most of it start-up.
+// 354); 1098 rows over 16 pages of 64 each, 553 us (128-row form: 1449), 8.3 TB/s of K/V tiles
+// mostly out of L2: no unit is near its limit there (L2 at 36% of its peak, DRAM 11%, tensor pipe
+// 7%), so what bounds it is the loads' latency with three tile pairs in flight and units that
+// are 8 tiles long; 7 sequences of up to 6 drafted tokens, 25 us, most of it start-up.
 #pragma once
 
 #include <cfloat>

@@ -304,7 +304,7 @@ attn_status_t attn_decode_splitkv_noalloc(const void *q, const void *k, const vo
  *   cu_q          int32 [B + 1] (written) exclusive prefix sum of new
  *   slot_map      int64 [T] (written) page * page_size + offset of every row's
  *                 token; -1 for rows of no sequence and tokens without a page
- *   B <= 8192 (ATTN_ERR_UNSUPPORTED); T >= 1 rows; num_free >= 1.
+ *   B <= 8192 (ATTN_ERR_UNSUPPORTED); 1 <= T <= 2^30 rows; num_free >= 1.
  *   A sequence whose lengths are negative or exceed its table gets no token
  *   (seq_lens = ctx clamped to the table); tokens past row T are cut off and do
  *   not count; a page past the end of the free list or outside [0, num_pages) is
@@ -356,7 +356,8 @@ size_t attn_fwd_paged_workspace_bytes(int d);
  *   lse  fp32 [T, Hq]      (written; natural log)
  *   causal 1: a token sees the keys up to its own position; 0: all seq_lens[b]
  *   keys. A row that sees no key gets O = 0, LSE = -inf.
- *   d in {64, 128}; Hq a multiple of Hkv with Hq / Hkv <= 128; T >= 1 rows;
+ *   d in {64, 128}; Hq a multiple of Hkv with Hq / Hkv <= 128; 1 <= T <= 2^30
+ *   rows; B <= 2^24;
  *   workspace 256-byte aligned, attn_fwd_paged_workspace_bytes(d) bytes.
  *   What a page holds past the sequence's last token never matters. Keys that
  *   cannot be read (bad table entries) are skipped. V of the cached tokens
@@ -382,11 +383,12 @@ size_t attn_page_select_workspace_bytes(int T, int Hkv, int max_pages_per_seq);
  * keep_last and those with the highest scores, num_sel in all (the lowest page first among
  * equal scores); fewer if it sees fewer.
  *
- *   k_bounds  bf16 [num_pages, Hkv, 2, d] (read; finite: a page whose score is
- *             NaN ranks above all others)
+ *   k_bounds  bf16 [num_pages, Hkv, 2, d] (read): a page whose score is NaN
+ *             ranks above all others
  *   sel       int32 [T, Hkv, num_sel] (written): logical pages, ascending, then -1
  *   num_sel >= 1, keep_first + keep_last <= num_sel, max_pages_per_seq <= 16384,
- *   Hq / Hkv <= 128 (ATTN_ERR_UNSUPPORTED beyond). Sums are taken in 64 bits.
+ *   Hq / Hkv <= 128 (ATTN_ERR_UNSUPPORTED beyond); T * Hkv and T * ceil(max_pages_per_seq / 64) <=
+ *   2^30. The choice is that of 64-bit sums.
  */
 attn_status_t attn_page_select(const void *q, const void *k_bounds, const int *block_table,
                                const int *cu_q, const int *seq_lens, int *sel, int B, int T,
