@@ -417,3 +417,66 @@ def test_first_call_of_a_thread(what):
     with ThreadPoolExecutor(1) as pool:
         pool.submit(call).result()
     assert m.attn_status() == 0
+
+
+FORMS = [([1, 1], 4), ([5, 2], 8), ([3, 90], 4), ([300], 2), ([2], 40)]   # 16, 32 columns, 128-row tiles
+
+
+@pytest.mark.parametrize("new,G", FORMS)
+@pytest.mark.parametrize("sparse", [False, True])
+def test_queries_that_are_not_finite_stay_in_their_rows(new, G, sparse):
+    """NaN and infinite query rows make NaN of their own outputs alone; those of padding rows of none."""
+    s = pu.make_step(new, [700, 40][:len(new)], 2 * G, 2, 64, 16, seed=G, pad=3)
+    sel = None
+    if sparse:
+        sel = torch.arange(6, dtype=torch.int32).expand(s.T, 2, 6).clone()
+        for b in range(s.B):
+            rows = slice(int(s.cu[b]), int(s.cu[b + 1]))
+            sel[rows][sel[rows] * 16 >= s.lens[b]] = -1
+    ref = pu.ref_attn(s, sel=sel)
+    end = int(s.cu[-1])
+    s.q[end:] = float("nan")
+    s.q[end + 1] = float("inf")
+    bad = torch.zeros((s.T, 2 * G), dtype=torch.bool)
+    for t, h, x in ((0, 0, float("nan")), (end - 1, 2 * G - 1, float("inf"))):
+        s.q[t, h, 3] = x
+        bad[t, h] = True
+    o, lse, status = _attn(s, sel=sel)
+    assert status == 0
+    assert (o[end:] == -77).all() and (lse[end:] == -77).all()
+    assert torch.isnan(o[bad]).all() and torch.isnan(lse[bad]).all()
+    good = ~bad
+    good[end:] = False
+    assert ((o[good].double() - ref[0][good]).abs() <= ref[2][good]).all()
+    assert ((lse[good].double() - ref[1][good]).abs() <= ref[3][good]).all()
+
+
+@pytest.mark.parametrize("new,G", FORMS)
+def test_keys_of_minus_infinity_weigh_nothing(new, G):
+    """Scores of -infinity among finite ones: as if those keys were not there. The first keys of a
+    sequence and the last whole tile before a row's own position, so that a tile can be all of them."""
+    s = pu.make_step(new, [700, 40][:len(new)], 2 * G, 2, 64, 16, seed=G + 1)
+    s.q[:, :, 0] = s.q[:, :, 0].abs() + 0.5
+    keep = [torch.ones(ln, dtype=torch.bool) for ln in s.lens]
+    keep[0][:140] = False
+    keep[0][256:512] = False
+    clean = [pu.seq_kv(s, b)[0] for b in range(s.B)]
+    for j in torch.nonzero(~keep[0])[:, 0].tolist():
+        s.kc[s.table[0, j // 16], :, j % 16, 0] = -float("inf")
+    o, lse, status = _attn(s)
+    assert status == 0
+    for b in range(s.B):
+        n, ln = s.new[b], s.lens[b]
+        v = pu.seq_kv(s, b)[1]
+        rows = slice(int(s.cu[b]), int(s.cu[b]) + n)
+        seen = (torch.arange(ln)[None] <= (ln - n + torch.arange(n))[:, None]) & keep[b]
+        for h in range(2 * G):
+            q, k, vv = s.q[rows, h].double(), clean[b][h // G], v[h // G]
+            score = torch.where(seen, q @ k.T * s.scale, -torch.inf)
+            want = torch.logsumexp(score, 1)
+            p = torch.exp(score - want[:, None])
+            # (the bounds of ref_attn)
+            e = torch.where(seen, q.abs() @ k.abs().T, 0.0).amax(1) * s.scale * 2 * 64 * 2.0 ** -24
+            tol = 2.0 ** -8 * (p @ vv).abs() + (2.0 ** -8 + 2 * e + 2.0 ** -18)[:, None] * (p @ vv.abs())
+            assert ((o[rows, h].double() - p @ vv).abs() <= tol).all()
+            assert ((lse[rows, h].double() - want).abs() <= e + 2.0 ** -18 * (1 + want.abs())).all()
