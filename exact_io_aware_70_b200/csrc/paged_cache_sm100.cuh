@@ -739,8 +739,9 @@ __global__ void __launch_bounds__(THREADS == 32 ? 128 : THREADS)
             }
         }
     }
-    if (blockIdx.x == 0)                                 // lengths and offsets out of range
-        for (int b = threadIdx.x; b < p.B; b += blockDim.x) bad = bad || paged_seq(p, b).bad;
+    // lengths and offsets out of range: a share of the sequences per block
+    for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < p.B; b += gridDim.x * blockDim.x)
+        bad |= paged_seq(p, b).bad;
     if (bad) atomicOr(&g_attn_status, kDevErrBadIndex);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (row.b < 0) return;                               // rows of no sequence stay as they were

@@ -480,3 +480,20 @@ def test_keys_of_minus_infinity_weigh_nothing(new, G):
             tol = 2.0 ** -8 * (p @ vv).abs() + (2.0 ** -8 + 2 * e + 2.0 ** -18)[:, None] * (p @ vv.abs())
             assert ((o[rows, h].double() - p @ vv).abs() <= tol).all()
             assert ((lse[rows, h].double() - want).abs() <= e + 2.0 ** -18 * (1 + want.abs())).all()
+
+
+@pytest.mark.parametrize("at", [0, 127, 128, 2999])
+def test_select_checks_every_sequence_of_a_long_batch(at):
+    """3000 sequences, of which one has a length out of range, and only a few rows among them."""
+    m = gpu_util.ea()
+    new = [1 if b % 500 == 0 else 0 for b in range(3000)]
+    s = pu.make_step(new, [b % 40 for b in range(3000)], 2, 1, 64, 16, seed=1, poison=False)
+    kb = pu.page_bounds(s.kc)
+    want = pu.ref_select(s, kb, 2, 0, 1)
+    sel, status = _select(s, kb, 2, 16, 0, 1)
+    assert status == 0 and torch.equal(sel, want)
+    s.seq[at] = -1
+    sel, status = _select(s, kb, 2, 16, 0, 1)
+    assert status == m.ATTN_ERR_BAD_INDEX
+    rows = [i for i, b in enumerate(range(0, 3000, 500)) if b != at]
+    assert torch.equal(sel[rows], want[rows])
